@@ -44,6 +44,8 @@ CCL_FLAG_DEBUG_DROP_FLAG = 0x1000
 CCL_FLAG_DEBUG_POISON = 0x2000
 CCL_I_RECV, CCL_I_SRCB, CCL_I_DSTA, CCL_I_SEND, CCL_I_LOCAL_IN = 0x1, 0x2, 0x4, 0x8, 0x10
 CCL_I_SKIP, CCL_I_NOFLAG = 0x20, 0x40
+CCL_ACT_NONE, CCL_ACT_RELU, CCL_ACT_GELU, CCL_ACT_GELU_TANH, CCL_ACT_SILU = range(5)
+CCL_LINEAR_UNALIGNED = 0x1
 
 
 class ccl_chunk_op(C.Structure):
@@ -112,6 +114,13 @@ class ccl_tune_report(C.Structure):
                 ("start_score", C.c_double)]
 
 
+class ccl_linear_desc(C.Structure):
+    _fields_ = [("dtype", C.c_int32), ("activation", C.c_int32), ("rows", C.c_int64), ("in_features", C.c_int64),
+                ("out_features", C.c_int64), ("experts", C.c_int32), ("flags", C.c_uint32), ("ld_x", C.c_int64),
+                ("ld_w", C.c_int64), ("ld_out", C.c_int64), ("ld_residual", C.c_int64), ("ld_preact", C.c_int64),
+                ("ld_dx", C.c_int64), ("ld_dw", C.c_int64)]
+
+
 ccl_tune_objective = C.CFUNCTYPE(C.c_double, C.POINTER(ccl_tune_point), C.c_void_p)
 
 
@@ -161,6 +170,21 @@ def _load():
         "ccl_stream_create_cu_masked": (C.c_int, [P(C.c_uint32), C.c_int, P(C.c_void_p)]),
         "ccl_stream_destroy": (C.c_int, [C.c_void_p]),
         "ccl_cu_probe": (C.c_int, [C.c_void_p, C.c_int, C.c_int, P(C.c_uint32)]),
+        "ccl_linear_workspace": (C.c_int64, [P(ccl_linear_desc), C.c_int, C.c_int]),
+        "ccl_linear": (C.c_int, [P(ccl_linear_desc)] + [C.c_void_p] * 7 + [C.c_size_t, C.c_void_p]),
+        "ccl_linear_backward": (C.c_int, [P(ccl_linear_desc)] + [C.c_void_p] * 8 + [C.c_size_t, C.c_void_p]),
+        "ccl_grouped_linear": (C.c_int, [P(ccl_linear_desc)] + [C.c_void_p] * 7 + [C.c_size_t, C.c_void_p]),
+        "ccl_grouped_linear_backward": (C.c_int, [P(ccl_linear_desc)] + [C.c_void_p] * 9 + [C.c_size_t, C.c_void_p]),
+        "ccl_expert_route_workspace": (C.c_int64, [C.c_int64, C.c_int, C.c_int]),
+        "ccl_expert_route": (C.c_int, [C.c_void_p, C.c_int64, C.c_int, C.c_int] + [C.c_void_p] * 4 +
+                             [C.c_size_t, C.c_void_p]),
+        "ccl_expert_dispatch": (C.c_int, [C.c_int, C.c_void_p, C.c_int64, C.c_void_p, C.c_int64, C.c_int, C.c_int64,
+                                          C.c_void_p, C.c_int64, C.c_void_p]),
+        "ccl_expert_combine": (C.c_int, [C.c_int, C.c_void_p, C.c_int64, C.c_void_p, C.c_void_p, C.c_int64, C.c_int,
+                                         C.c_int64, C.c_void_p, C.c_int64, C.c_void_p]),
+        "ccl_expert_combine_backward": (C.c_int, [C.c_int, C.c_void_p, C.c_int64, C.c_void_p, C.c_int64, C.c_void_p,
+                                                  C.c_void_p, C.c_void_p, C.c_int64, C.c_int, C.c_int64, C.c_void_p,
+                                                  C.c_int64, C.c_void_p, C.c_void_p]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -175,7 +199,9 @@ EXPORTED = ("ccl_version", "ccl_error_string", "ccl_last_error_detail", "ccl_pla
             "ccl_plan_destroy", "ccl_plan_info", "ccl_plan_bytes", "ccl_plan_export", "ccl_plan_check",
             "ccl_plan_status", "ccl_plan_read_trace", "ccl_plan_link_busy", "ccl_tune_coordinate_descent", "ccl_tune",
             "ccl_copy_probe", "ccl_litmus_message_passing", "ccl_hop_probe", "ccl_stream_create_cu_masked",
-            "ccl_stream_destroy", "ccl_cu_probe")
+            "ccl_stream_destroy", "ccl_cu_probe", "ccl_linear_workspace", "ccl_linear", "ccl_linear_backward",
+            "ccl_grouped_linear", "ccl_grouped_linear_backward", "ccl_expert_route_workspace", "ccl_expert_route",
+            "ccl_expert_dispatch", "ccl_expert_combine", "ccl_expert_combine_backward")
 
 
 def lib():
@@ -353,3 +379,67 @@ def ccl_cu_probe(stream: int, nblocks: int, hold_us: int = 50):
         x, hw = out[2 * b], out[2 * b + 1]
         res.append((x, (hw >> 13) & 7, (hw >> 12) & 1, (hw >> 8) & 15))
     return res
+
+
+# ---- products and row exchange: device addresses as ints, 0 for NULL -------------------
+def ccl_linear_workspace(desc: ccl_linear_desc, grouped: bool, backward: bool) -> int:
+    v = _lib.ccl_linear_workspace(C.byref(desc), int(bool(grouped)), int(bool(backward)))
+    if v < 0:
+        _check(int(v), "ccl_linear_workspace")
+    return int(v)
+
+
+def ccl_linear(desc: ccl_linear_desc, x: int, w: int, bias: int, residual: int, out: int, preact: int, workspace: int,
+               workspace_bytes: int, stream: int = 0) -> None:
+    _check(_lib.ccl_linear(C.byref(desc), x, w, bias, residual, out, preact, workspace, workspace_bytes, stream),
+           "ccl_linear")
+
+
+def ccl_linear_backward(desc: ccl_linear_desc, dout: int, x: int, w: int, preact: int, dx: int, dw: int, dbias: int,
+                        workspace: int, workspace_bytes: int, stream: int = 0) -> None:
+    _check(_lib.ccl_linear_backward(C.byref(desc), dout, x, w, preact, dx, dw, dbias, workspace, workspace_bytes,
+                                    stream), "ccl_linear_backward")
+
+
+def ccl_grouped_linear(desc: ccl_linear_desc, offsets: int, x: int, w: int, bias: int, out: int, preact: int,
+                       workspace: int, workspace_bytes: int, stream: int = 0) -> None:
+    _check(_lib.ccl_grouped_linear(C.byref(desc), offsets, x, w, bias, out, preact, workspace, workspace_bytes,
+                                   stream), "ccl_grouped_linear")
+
+
+def ccl_grouped_linear_backward(desc: ccl_linear_desc, offsets: int, dout: int, x: int, w: int, preact: int, dx: int,
+                                dw: int, dbias: int, workspace: int, workspace_bytes: int, stream: int = 0) -> None:
+    _check(_lib.ccl_grouped_linear_backward(C.byref(desc), offsets, dout, x, w, preact, dx, dw, dbias, workspace,
+                                            workspace_bytes, stream), "ccl_grouped_linear_backward")
+
+
+def ccl_expert_route_workspace(tokens: int, choices: int, experts: int) -> int:
+    v = _lib.ccl_expert_route_workspace(tokens, choices, experts)
+    if v < 0:
+        _check(int(v), "ccl_expert_route_workspace")
+    return int(v)
+
+
+def ccl_expert_route(ids: int, tokens: int, choices: int, experts: int, offsets: int, positions: int, slots: int,
+                     workspace: int, workspace_bytes: int, stream: int = 0) -> None:
+    _check(_lib.ccl_expert_route(ids, tokens, choices, experts, offsets, positions, slots, workspace, workspace_bytes,
+                                 stream), "ccl_expert_route")
+
+
+def ccl_expert_dispatch(dtype: int, x: int, ld_x: int, slots: int, tokens: int, choices: int, width: int, rows: int,
+                        ld_rows: int, stream: int = 0) -> None:
+    _check(_lib.ccl_expert_dispatch(dtype, x, ld_x, slots, tokens, choices, width, rows, ld_rows, stream),
+           "ccl_expert_dispatch")
+
+
+def ccl_expert_combine(dtype: int, h: int, ld_h: int, positions: int, gates: int, tokens: int, choices: int,
+                       width: int, out: int, ld_out: int, stream: int = 0) -> None:
+    _check(_lib.ccl_expert_combine(dtype, h, ld_h, positions, gates, tokens, choices, width, out, ld_out, stream),
+           "ccl_expert_combine")
+
+
+def ccl_expert_combine_backward(dtype: int, dout: int, ld_dout: int, h: int, ld_h: int, positions: int, slots: int,
+                                gates: int, tokens: int, choices: int, width: int, dh: int, ld_dh: int, dgates: int,
+                                stream: int = 0) -> None:
+    _check(_lib.ccl_expert_combine_backward(dtype, dout, ld_dout, h, ld_h, positions, slots, gates, tokens, choices,
+                                            width, dh, ld_dh, dgates, stream), "ccl_expert_combine_backward")

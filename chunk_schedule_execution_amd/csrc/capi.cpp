@@ -32,20 +32,12 @@ int set_error(int code, const std::string& msg) {
 
 template <typename F>
 int guarded(F&& f) {
-  try {
-    return f();
-  } catch (const Error& e) {
-    return set_error(e.code, e.what());
-  } catch (const std::bad_alloc&) {
-    return set_error(CCL_ERR_OUT_OF_RESOURCES, "host allocation failed");
-  } catch (const std::exception& e) {
-    return set_error(CCL_ERR_INTERNAL, e.what());
-  } catch (...) {
-    return set_error(CCL_ERR_INTERNAL, "unknown exception");
-  }
+  return api_guarded(std::forward<F>(f));
 }
 
 }  // namespace
+
+int ccl::api_error(int code, const std::string& msg) { return set_error(code, msg); }
 
 struct ccl_plan {
   HostPlan hp;

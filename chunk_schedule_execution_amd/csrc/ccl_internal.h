@@ -2,9 +2,11 @@
 #pragma once
 
 #include <cstdint>
+#include <new>
 #include <stdexcept>
 #include <string>
 #include <set>
+#include <utility>
 #include <vector>
 
 #include "../../include/ccl.h"
@@ -17,6 +19,24 @@ struct Error : std::runtime_error {
   Error(int c, const std::string& m) : std::runtime_error(m), code(c) {}
 };
 [[noreturn]] void fail(int code, const std::string& msg);
+
+// Every C entry point runs its body through api_guarded: no exception crosses the
+// boundary, and the calling thread's error text is set (api_error, capi.cpp).
+int api_error(int code, const std::string& msg);
+template <typename F>
+int api_guarded(F&& f) {
+  try {
+    return f();
+  } catch (const Error& e) {
+    return api_error(e.code, e.what());
+  } catch (const std::bad_alloc&) {
+    return api_error(CCL_ERR_OUT_OF_RESOURCES, "host allocation failed");
+  } catch (const std::exception& e) {
+    return api_error(CCL_ERR_INTERNAL, e.what());
+  } catch (...) {
+    return api_error(CCL_ERR_INTERNAL, "unknown exception");
+  }
+}
 
 // Chunk geometry shared by the lowering, byte accounting and the plan checker:
 // chunk j covers [floor(j*N/C), floor((j+1)*N/C)); instance i of k takes

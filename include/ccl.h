@@ -533,6 +533,126 @@ int ccl_stream_destroy(void* stream);
  */
 int ccl_cu_probe(void* stream, int nblocks, int hold_us, uint32_t* out);
 
+/* ---- products and row exchange of sharded layers ---------------------------
+ *
+ * What a rank computes next to its collectives: the product of a tensor-parallel layer
+ * between its AllGather and AllReduce, the products of the rank's experts between the
+ * two AllToAlls of an expert-parallel layer, and the row exchange that packs and unpacks
+ * those AllToAlls.
+ *
+ * Common rules:
+ *   - dtype is CCL_F32 or CCL_BF16 and holds for every floating tensor of a call (gates
+ *     and their gradients are always fp32). Sums are taken in fp32 and rounded once to
+ *     the dtype (nearest-even).
+ *   - Matrices are row-major; ld_* is the distance between rows in elements (0 = packed).
+ *     Base pointers are aligned to their element. Inputs must not overlap outputs.
+ *   - A call enqueues its kernels on `stream` and returns; it allocates nothing,
+ *     synchronizes nothing and may be captured into a graph. The workspace (device
+ *     memory, 16-byte aligned, at least the bytes its query returns, contents arbitrary)
+ *     belongs to the call until the stream passes it; calls on different streams need
+ *     workspaces of their own.
+ *   - The same inputs give the same bits (no atomics on floating values).
+ *   - Device-side index arrays are bounds-checked in the kernels (each call says how), so
+ *     bad ones give wrong values but never an access outside the tensors.
+ */
+#define CCL_ACT_NONE 0
+#define CCL_ACT_RELU 1      /* max(z, 0); slope 0 at 0; a NaN stays one */
+#define CCL_ACT_GELU 2      /* z (1 + erf(z / sqrt 2)) / 2 */
+#define CCL_ACT_GELU_TANH 3 /* z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2 */
+#define CCL_ACT_SILU 4      /* z / (1 + exp(-z)) */
+
+#define CCL_LINEAR_UNALIGNED 0x1u /* some matrix base pointer is not 16-byte aligned */
+
+typedef struct {
+  int32_t dtype;         /* CCL_F32 or CCL_BF16 */
+  int32_t activation;    /* CCL_ACT_* */
+  int64_t rows;          /* M >= 0: rows of x and out, below 2^31 */
+  int64_t in_features;   /* K in 1 .. 2^20: row length of x and of the weights */
+  int64_t out_features;  /* N in 1 .. 2^20: row length of out, rows of one weight matrix */
+  int32_t experts;       /* grouped calls: E in 1 .. 4096 weight matrices; other calls: 0 or 1 */
+  uint32_t flags;        /* CCL_LINEAR_UNALIGNED */
+  int64_t ld_x, ld_w, ld_out, ld_residual, ld_preact; /* ld_out is also dout's; each at most 2^22 */
+  int64_t ld_dx, ld_dw;  /* backward only */
+} ccl_linear_desc;
+
+/*
+ * Bytes of workspace a call with this descriptor needs (0: none, the pointer may be
+ * NULL). grouped / backward: nonzero for the grouped calls / the backward calls. Returns
+ * a negative status on a bad descriptor.
+ */
+int64_t ccl_linear_workspace(const ccl_linear_desc* desc, int grouped, int backward);
+
+/*
+ * out = act(z) + residual with z = x w^T + bias: x rows x in_features, w out_features x
+ * in_features, bias out_features or NULL, residual rows x out_features or NULL, out rows
+ * x out_features, preact NULL or rows x out_features (receives z). The activation sees z
+ * in fp32, not its rounding in preact. rows = 0 enqueues nothing.
+ * Errors: INVALID_ARGUMENT (sizes, strides shorter than a row, null or misaligned
+ * pointers, a workspace that is too small), UNSUPPORTED (dtype, activation), HIP.
+ */
+int ccl_linear(const ccl_linear_desc* desc, const void* x, const void* w, const void* bias, const void* residual,
+               void* out, void* preact, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Gradients: with dz = dout act'(preact), dx = dz w, dw = dz^T x, dbias = column sums of
+ * dz (the residual's gradient is dout itself). Any of dx, dw, dbias may be NULL; preact
+ * may be NULL when the activation is CCL_ACT_NONE, w when dx is NULL, x when dw is NULL.
+ * With rows = 0, dw and dbias are set to zero. dz is rounded to the dtype for the
+ * products (as a stored gradient is), the bias sums take it unrounded. Errors: as above.
+ */
+int ccl_linear_backward(const ccl_linear_desc* desc, const void* dout, const void* x, const void* w,
+                        const void* preact, void* dx, void* dw, void* dbias, void* workspace, size_t workspace_bytes,
+                        void* stream);
+
+/*
+ * The same by groups of rows: rows offsets[e] .. offsets[e + 1] - 1 of x are multiplied
+ * by expert e's matrix, w + e out_features ld_w, and get its bias, bias + e out_features.
+ * offsets: device array of experts + 1 values; offsets[0] is taken as 0, a value outside
+ * [0, rows] is clamped and one below an earlier value counts as that value. A group may
+ * be empty. Rows from offsets[experts] on belong to no group: out, preact and dx are set
+ * to zero there. In the backward call every expert has its own matrix in dw (e
+ * out_features ld_dw) and row in dbias; both are zero for an empty group.
+ */
+int ccl_grouped_linear(const ccl_linear_desc* desc, const int32_t* offsets, const void* x, const void* w,
+                       const void* bias, void* out, void* preact, void* workspace, size_t workspace_bytes,
+                       void* stream);
+int ccl_grouped_linear_backward(const ccl_linear_desc* desc, const int32_t* offsets, const void* dout, const void* x,
+                                const void* w, const void* preact, void* dx, void* dw, void* dbias, void* workspace,
+                                size_t workspace_bytes, void* stream);
+
+/*
+ * Route `tokens` tokens with `choices` experts each: ids[t * choices + j] is token t's
+ * j-th expert; an id outside [0, experts) is served elsewhere and gets no row. A choice's
+ * slot is its index in ids. Rows are ordered by expert, and by slot within an expert
+ * (a stable counting sort): offsets (experts + 1 values) delimits the experts' rows,
+ * positions[slot] is the slot's row or -1, slots[row] the row's slot or -1 for the rows
+ * from offsets[experts] on. experts in 1 .. 1024, tokens * choices below 2^31 (0 only
+ * writes offsets). Errors: INVALID_ARGUMENT, HIP.
+ */
+int64_t ccl_expert_route_workspace(int64_t tokens, int choices, int experts);
+int ccl_expert_route(const int32_t* ids, int64_t tokens, int choices, int experts, int32_t* offsets,
+                     int32_t* positions, int32_t* slots, void* workspace, size_t workspace_bytes, void* stream);
+
+/* rows[i] = x[slots[i] / choices] for i < tokens * choices, zeros where slots[i] is not a
+ * slot. x: tokens rows of `width` elements, rows: tokens * choices. The gradient of x is
+ * ccl_expert_combine of the rows' gradients without gates. */
+int ccl_expert_dispatch(int dtype, const void* x, int64_t ld_x, const int32_t* slots, int64_t tokens, int choices,
+                        int64_t width, void* rows, int64_t ld_rows, void* stream);
+
+/* out[t] = sum over j of gates[t * choices + j] h[positions[t * choices + j]], added in
+ * the order of j in fp32; a position that is not a row of h (tokens * choices rows) adds
+ * nothing. gates: fp32, or NULL for ones. */
+int ccl_expert_combine(int dtype, const void* h, int64_t ld_h, const int32_t* positions, const float* gates,
+                       int64_t tokens, int choices, int64_t width, void* out, int64_t ld_out, void* stream);
+
+/* Gradients of the combine: dh[i] = gates[slots[i]] dout[slots[i] / choices] (zeros where
+ * slots[i] is not a slot; gates NULL for ones) and dgates[slots[i]] = <h[i], dout[slots[i]
+ * / choices]>, zero for a slot whose position is not a row. positions and slots are one
+ * route's. dh or dgates (then h too) may be NULL. */
+int ccl_expert_combine_backward(int dtype, const void* dout, int64_t ld_dout, const void* h, int64_t ld_h,
+                                const int32_t* positions, const int32_t* slots, const float* gates, int64_t tokens,
+                                int choices, int64_t width, void* dh, int64_t ld_dh, float* dgates, void* stream);
+
 /* ---- errors --------------------------------------------------------------- */
 const char* ccl_error_string(int status);
 const char* ccl_last_error_detail(void);
