@@ -1,0 +1,391 @@
+// The tiled product kernel for gfx950: operands whose rows lie on the 16-byte grid.
+#pragma once
+
+#include "products_device.h"
+
+namespace ccl {
+namespace prod {
+namespace {
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) void* lds_ptr;
+
+// ---- operand tiles in LDS -------------------------------------------------------------
+// A step of the summed dimension is 128 bytes of a row: 64 bf16 or 32 fp32 values. Tiles
+// come straight from memory by 16-byte buffer loads into LDS (no registers in between),
+// whose destination is lane-linear, so the layouts below permute the source addresses.
+//
+// Stored by rows (ByK false): tile [R rows][8 chunks of 16 bytes], chunk c of row r at
+// position c ^ (r & 7). A matrix instruction's lanes read chunk c of 16 neighbouring
+// rows: any 8 of them hit 8 different positions, all 128 bytes of the banks.
+//
+// Stored by k (ByK true): tile [step rows of k][R values]. bf16: the transposing read
+// takes from 16 lanes 4 rows of k by 16 values and hands each lane 4 k values of its
+// column; rows are R * 2 bytes apart, so the 32-byte windows are permuted by (k & 3).
+// fp32: lanes read single values of 4 rows four apart; 64-byte windows permuted by
+// (k >> 2) & 3.
+//
+// Which k values a lane of a matrix instruction holds is free as long as both operands
+// agree: lane group g = lane >> 4 takes the step's bytes [64 h + 16 g, 64 h + 16 g + 16)
+// of half h, for both layouts.
+template <typename T, bool ByK, int R, int Threads>
+struct OperandTile {
+  static constexpr int kSize = sizeof(T), kStep = 128 / kSize, kVec = 16 / kSize;
+  static constexpr int kLoads = R * 8 / Threads;
+  static constexpr int kChunks = ByK ? R / kVec : 8;  // per stored row
+  static_assert(kLoads * Threads == R * 8 && kLoads >= 1, "whole loads");
+
+  const char* base;  // first value of the tile at the current step
+  int64_t step_bytes;
+  int64_t records;   // readable bytes from base (by rows), or of the whole rest (by k)
+  int64_t ld_bytes;
+  int voff[kLoads];
+  int kc;  // by rows: first k value of this lane's chunk
+
+  // row: first row (or column) of the tile, end: one past the last readable one; k_lo, k_hi:
+  // the summed range.
+  __device__ inline void init(const T* p, int64_t ld, int64_t row, int64_t end, int64_t k_lo, int64_t k_hi) {
+    const int tid = threadIdx.x;
+    ld_bytes = ld * kSize;
+    if constexpr (ByK) {
+      base = reinterpret_cast<const char*>(p + k_lo * ld + row);
+      step_bytes = ld_bytes * kStep;
+      records = (end - row) * kSize;  // of the last row
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const int q = i * Threads + tid, k = q / kChunks, c = (q % kChunks) ^ swizzle(k);
+        voff[i] = int(k * ld_bytes) + c * 16;
+      }
+    } else {
+      base = reinterpret_cast<const char*>(p + row * ld + k_lo);
+      step_bytes = 128;
+      records = (min(int64_t(R), end - row) - 1) * ld_bytes + (k_hi - k_lo) * kSize;
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const int q = i * Threads + tid, r = q / 8, c = (q % 8) ^ (r & 7);
+        voff[i] = int(r * ld_bytes) + c * 16;
+        kc = c * kVec;  // the same for every i: rows differ by multiples of 8
+      }
+    }
+  }
+
+  static __device__ inline int swizzle(int k) { return kSize == 2 ? (k & 3) << 1 : ((k >> 2) & 3) << 2; }
+
+  // Starts the loads of the step whose `left` summed values (>= 1) remain, into `lds`, and
+  // moves on to the next step. Out of range reads give zeros.
+  __device__ inline void load(T* lds, int64_t left) {
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t rest = ByK ? (min(int64_t(kStep), left) - 1) * ld_bytes + records : records;
+    const __amdgpu_buffer_rsrc_t rsrc =
+        __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base), 0, int(rest), 0x00020000);
+    // by rows, the last step: chunks behind the row's end would be the next row's values
+    const bool out = !ByK && left < kStep && kc >= left;
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          rsrc, (lds_ptr)(reinterpret_cast<char*>(lds) + (i * Threads + wave * 64) * 16), 16, out ? -1 : voff[i], 0, 0,
+          0);
+    base += step_bytes;
+    if (!ByK) records -= 128;
+  }
+};
+
+// A wave's reads of one operand: F fragments of 16 rows from row r0 of the tile.
+template <typename T, bool ByK, int R, int F>
+struct FragmentReader {
+  static constexpr int kSize = sizeof(T);
+  static constexpr int kOffsets = ByK ? (F < 4 ? F : 4) : 2;
+  static_assert(!ByK || F <= 4 || F % 4 == 0, "whole windows");
+  int off[kOffsets];
+
+  __device__ inline void init(int r0) {
+    const int lane = threadIdx.x & 63, g = lane >> 4;
+    if constexpr (!ByK) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) off[h] = (r0 + (lane & 15)) * 128 + (((h * 4 + g) ^ (lane & 7)) * 16);
+    } else if constexpr (kSize == 2) {
+      const int j = (lane >> 2) & 3;  // row of k within the lane group's 4
+#pragma unroll
+      for (int i = 0; i < kOffsets; ++i) {
+        const int chunk = ((r0 / 8 + 2 * i) ^ (j << 1)) + ((lane & 3) >> 1);
+        off[i] = (g * 8 + j) * (R * 2) + chunk * 16 + (lane & 1) * 8;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kOffsets; ++i) {
+        const int chunk = ((r0 / 4 + 4 * i) ^ (g << 2)) + ((lane & 15) >> 2);
+        off[i] = g * 4 * (R * 4) + chunk * 16 + (lane & 3) * 4;
+      }
+    }
+  }
+
+  // Half h of fragment i: 16 bytes of k values per lane.
+  __device__ inline auto read(const T* lds, int i, int h) const {
+    const char* p = reinterpret_cast<const char*>(lds);
+    if constexpr (!ByK) {
+      typedef T vec __attribute__((ext_vector_type(16 / sizeof(T))));
+      return *reinterpret_cast<const vec*>(p + off[h] + i * 2048);
+    } else if constexpr (kSize == 2) {
+      const char* at = p + off[i & 3] + (i >> 2) * 128 + h * 32 * (R * 2);
+      typedef __attribute__((address_space(3))) s16x4* tr_ptr;
+      const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((tr_ptr)at);
+      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((tr_ptr)(at + 4 * (R * 2)));
+      typedef short s16x8 __attribute__((ext_vector_type(8)));
+      const s16x8 v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+      return __builtin_bit_cast(bf16x8, v);
+    } else {
+      const char* at = p + off[i & 3] + (i >> 2) * 256 + h * 16 * (R * 4);
+      f32x4 v;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v[q] = *reinterpret_cast<const float*>(at + q * (R * 4));
+      return v;
+    }
+  }
+};
+
+__device__ inline f32x4 multiply(bf16x8 x, bf16x8 y, f32x4 acc) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, y, acc, 0, 0, 0);
+}
+__device__ inline f32x4 multiply(f32x4 x, f32x4 y, f32x4 acc) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(x[q], y[q], acc, 0, 0, 0);
+  return acc;
+}
+
+// ---- results -----------------------------------------------------------------------------
+// 8 neighbouring values of a row; `vec`: the row lies on the 16-byte grid; `n`: how many of
+// them exist.
+template <typename T>
+__device__ inline void load8(const T* p, bool vec, int n, float* v) {
+  if (vec && n >= 8) {
+    constexpr int V = 16 / int(sizeof(T));
+    typedef T pack __attribute__((ext_vector_type(V)));
+#pragma unroll
+    for (int h = 0; h < 8 / V; ++h) {
+      const pack x = reinterpret_cast<const pack*>(p)[h];
+#pragma unroll
+      for (int q = 0; q < V; ++q) v[h * V + q] = widen(x[q]);
+    }
+  } else {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) v[q] = q < n ? widen(p[q]) : 0.0f;
+  }
+}
+template <typename T>
+__device__ inline void store8(T* p, bool vec, int n, const float* v) {
+  if (vec && n >= 8) {
+    constexpr int V = 16 / int(sizeof(T));
+    typedef T pack __attribute__((ext_vector_type(V)));
+#pragma unroll
+    for (int h = 0; h < 8 / V; ++h) {
+      pack x;
+#pragma unroll
+      for (int q = 0; q < V; ++q) x[q] = narrow<T>(v[h * V + q]);
+      reinterpret_cast<pack*>(p)[h] = x;
+    }
+  } else {
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      if (q < n) p[q] = narrow<T>(v[q]);
+  }
+}
+// The activation of 8 values: the branch is taken once for them.
+__device__ inline void act8(float* v, int act) {
+#define CCL_ACT8(A)                                            \
+  case A:                                                      \
+    _Pragma("unroll") for (int q = 0; q < 8; ++q) v[q] = act_value(v[q], A); \
+    break;
+  switch (act) {
+    CCL_ACT8(CCL_ACT_RELU)
+    CCL_ACT8(CCL_ACT_GELU)
+    CCL_ACT8(CCL_ACT_GELU_TANH)
+    CCL_ACT8(CCL_ACT_SILU)
+    default: break;
+  }
+#undef CCL_ACT8
+}
+
+__device__ inline void steps_arrived() {
+  __builtin_amdgcn_s_waitcnt(0x0F70);  // all of this wave's loads into LDS
+  __syncthreads();
+}
+
+// ---- the kernel ---------------------------------------------------------------------------
+// BM x BN values per workgroup, WM x WN waves, each (BM / WM) x (BN / WN) by matrix
+// instructions of 16 x 16. Two LDS buffers: the loads of a step run while the step before
+// is multiplied; one barrier per step orders both directions.
+template <typename T, bool AByK, bool BByK, int BM, int BN, int WM, int WN>
+__device__ inline void product_tile(const ProductArgs& g, ProductMode mode, int tiles_m, int tiles_n) {
+  constexpr int Threads = WM * WN * 64, FM = BM / WM / 16, FN = BN / WN / 16;
+  constexpr int kStep = 128 / int(sizeof(T));
+  constexpr int kTile = kStep;  // values per row of a stored tile
+  __shared__ __attribute__((aligned(1024))) T a0[BM * kTile];
+  __shared__ __attribute__((aligned(1024))) T b0[BN * kTile];
+  __shared__ __attribute__((aligned(1024))) T a1[BM * kTile];
+  __shared__ __attribute__((aligned(1024))) T b1[BN * kTile];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const T* A = static_cast<const T*>(g.a);
+  const T* B = static_cast<const T*>(g.b);
+  T* C = static_cast<T*>(g.c);
+  // quotients are computed in vector registers: uniform() brings them back
+  const int tile = blockIdx.x;
+  const int band = uniform(tile / tiles_n);
+  const int64_t col = int64_t(tile - band * tiles_n) * BN;
+  int group = 0;
+  int64_t row = 0, m_end = g.m, k_lo = 0, k_hi = g.k;
+  if (mode == kRaggedK) {
+    group = uniform(band / tiles_m);
+    row = int64_t(band - group * tiles_m) * BM;
+    group_bounds(g.offsets, g.k, group, k_lo, k_hi);
+    C += group * g.c_stride;
+  } else {
+    const RowTile t = find_tile(g.offsets, g.groups, g.m, BM, band, true);
+    if (t.group < 0) return;
+    group = uniform(t.group);
+    row = t.row;
+    m_end = t.end;
+    if (group == g.groups) k_hi = 0;  // rows of no group: zeros
+    else B += group * g.b_stride;
+  }
+  const bool nothing = mode == kRaggedM && group == g.groups;
+  row = uniform(int(row));  // row counts are below 2^31
+  m_end = uniform(int(m_end));
+  k_lo = uniform(int(k_lo));
+  k_hi = uniform(int(k_hi));
+
+  f32x4 acc[FM][FN] = {};
+  const int wm = wave / WN * (BM / WM), wn = wave % WN * (BN / WN);
+  if (k_lo < k_hi) {
+    OperandTile<T, AByK, BM, Threads> ta;
+    OperandTile<T, BByK, BN, Threads> tb;
+    ta.init(A, g.lda, row, m_end, k_lo, k_hi);
+    tb.init(B, g.ldb, col, g.n, k_lo, k_hi);
+    FragmentReader<T, AByK, BM, FM> ra;
+    FragmentReader<T, BByK, BN, FN> rb;
+    ra.init(wm);
+    rb.init(wn);
+    auto compute = [&](const T* la, const T* lb) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        decltype(rb.read(lb, 0, 0)) fb[FN];
+#pragma unroll
+        for (int j = 0; j < FN; ++j) fb[j] = rb.read(lb, j, h);
+#pragma unroll
+        for (int i = 0; i < FM; ++i) {
+          const auto fa = ra.read(la, i, h);
+#pragma unroll
+          for (int j = 0; j < FN; ++j) acc[i][j] = multiply(fb[j], fa, acc[i][j]);
+        }
+      }
+    };
+    int64_t left = k_hi - k_lo;
+    ta.load(a0, left);
+    tb.load(b0, left);
+    for (; left > 0; left -= 2 * kStep) {
+      steps_arrived();
+      if (left > kStep) {
+        ta.load(a1, left - kStep);
+        tb.load(b1, left - kStep);
+      }
+      compute(a0, b0);
+      if (left <= kStep) break;
+      steps_arrived();
+      if (left > 2 * kStep) {
+        ta.load(a0, left - 2 * kStep);
+        tb.load(b0, left - 2 * kStep);
+      }
+      compute(a1, b1);
+    }
+    __syncthreads();
+  }
+
+  // Results go through LDS, a wave's 16 (or 8) KiB at a time and to itself alone, so that
+  // rows are read and written in 16-byte vectors and the epilogue's code exists once.
+  constexpr int WTN = BN / WN, kChunks = WTN / 4;        // 16-byte chunks of fp32 per row
+  constexpr int kLanesPerRow = WTN / 8, kRowsPerPass = 64 / kLanesPerRow;
+  constexpr int kStage = 2;                              // fragments of rows per stage
+  float* const stage = reinterpret_cast<float*>(wave < WM * WN / 2 ? a0 : a1) + (wave % (WM * WN / 2)) * (kStage * 16 * WTN);
+  static_assert(kStage * 16 * WTN * 4 * (WM * WN / 2) <= BM * 128, "a wave's stage fits");
+  const T* bias = g.bias && !nothing ? static_cast<const T*>(g.bias) + group * g.bias_stride : nullptr;
+  const T* residual = static_cast<const T*>(g.residual);
+  T* preact = static_cast<T*>(g.preact);
+  const int64_t c = col + wn + (lane % kLanesPerRow) * 8;
+  const int n = int(min(int64_t(8), g.n - c));
+  const bool vec_c = g.ldc * sizeof(T) % 16 == 0 && reinterpret_cast<uintptr_t>(C) % 16 == 0;
+  const bool vec_r = g.ldr * sizeof(T) % 16 == 0 && reinterpret_cast<uintptr_t>(residual) % 16 == 0;
+  const bool vec_p = g.ldp * sizeof(T) % 16 == 0 && reinterpret_cast<uintptr_t>(preact) % 16 == 0;
+  float bv[8] = {};
+  if (bias && n > 0) load8(bias + c, false, n, bv);
+#pragma unroll
+  for (int i0 = 0; i0 < FM; i0 += kStage) {
+#pragma unroll
+    for (int i = 0; i < kStage; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; ++j) {
+        const int r = i * 16 + (lane & 15), chunk = j * 4 + (lane >> 4);
+        *reinterpret_cast<f32x4*>(stage + r * WTN + ((chunk ^ r) % kChunks) * 4) = acc[i0 + i][j];
+      }
+    __builtin_amdgcn_wave_barrier();
+#pragma nounroll
+    for (int r = lane / kLanesPerRow; r < kStage * 16; r += kRowsPerPass) {
+      const int64_t at = row + wm + i0 * 16 + r;
+      if (at >= m_end || n <= 0) continue;
+      const int chunk = (lane % kLanesPerRow) * 2;
+      float v[8];
+      *reinterpret_cast<f32x4*>(v) = *reinterpret_cast<const f32x4*>(stage + r * WTN + ((chunk ^ r) % kChunks) * 4);
+      *reinterpret_cast<f32x4*>(v + 4) =
+          *reinterpret_cast<const f32x4*>(stage + r * WTN + (((chunk + 1) ^ r) % kChunks) * 4);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) v[q] += bv[q];
+      if (preact) store8(preact + at * g.ldp + c, vec_p, n, v);
+      if (!nothing) act8(v, g.act);
+      if (residual) {
+        float w[8];
+        load8(residual + at * g.ldr + c, vec_r, n, w);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) v[q] += w[q];
+      }
+      store8(C + at * g.ldc + c, vec_c, n, v);
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
+// Two waves per SIMD: half of the registers each.
+template <typename T, bool AByK, bool BByK, int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(WM* WN * 64, 2) void product_tile_kernel(ProductArgs g, ProductMode mode, int tiles_m,
+                                                                      int tiles_n) {
+  product_tile<T, AByK, BByK, BM, BN, WM, WN>(g, mode, tiles_m, tiles_n);
+}
+
+template <typename T, int BM, int BN, int WM, int WN>
+int launch_tile(bool a_by_k, bool b_by_k, ProductMode mode, const ProductArgs& g, hipStream_t s, std::string* err) {
+  const int64_t tiles_n = (g.n + BN - 1) / BN, tiles_m = (g.m + BM - 1) / BM;
+  const int64_t grid = mode == kRaggedK ? g.groups * tiles_m * tiles_n
+                       : mode == kRaggedM ? (tiles_m + g.groups) * tiles_n : tiles_m * tiles_n;
+  if (grid > 0x7fffffff) {
+    *err = "product: more than 2^31 tiles";
+    return CCL_ERR_INVALID_ARGUMENT;
+  }
+  if (grid == 0) return CCL_OK;
+  auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3(unsigned(grid)), dim3(WM * WN * 64), 0, s, g, mode, int(tiles_m), int(tiles_n));
+  };
+  if (a_by_k && b_by_k) go(product_tile_kernel<T, true, true, BM, BN, WM, WN>);
+  else if (b_by_k) go(product_tile_kernel<T, false, true, BM, BN, WM, WN>);
+  else go(product_tile_kernel<T, false, false, BM, BN, WM, WN>);
+  const hipError_t e = hipGetLastError();
+  if (e == hipSuccess) return CCL_OK;
+  *err = std::string("product launch: ") + hipGetErrorString(e);
+  return CCL_ERR_HIP;
+}
+
+}  // namespace
+
+// Defined with their kernels in product_tile_bf16.hip and product_tile_f32.hip.
+int launch_tile_bf16(bool a_by_k, bool b_by_k, ProductMode mode, const ProductArgs& g, hipStream_t s, std::string* err);
+int launch_tile_f32(bool a_by_k, bool b_by_k, ProductMode mode, const ProductArgs& g, hipStream_t s, std::string* err);
+
+}  // namespace prod
+}  // namespace ccl

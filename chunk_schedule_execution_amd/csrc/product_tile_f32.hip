@@ -1,0 +1,13 @@
+// fp32 instances of the tiled product kernel.
+#include "product_tile.h"
+
+namespace ccl {
+namespace prod {
+
+int launch_tile_f32(bool a_by_k, bool b_by_k, ProductMode mode, const ProductArgs& g, hipStream_t s,
+                    std::string* err) {
+  return launch_tile<float, 128, 128, 2, 2>(a_by_k, b_by_k, mode, g, s, err);
+}
+
+}  // namespace prod
+}  // namespace ccl

@@ -1,6 +1,6 @@
 // Products beside the collectives for gfx950: C = act(A B^T + bias) + residual, plain or
 // grouped by expert with ragged sizes, for the forward pass and both gradients.
-#include "products_device.h"
+#include "product_tile.h"
 
 namespace ccl {
 namespace prod {
@@ -197,6 +197,12 @@ __global__ __launch_bounds__(256) void fill_zero_kernel(unsigned char* p, int64_
   for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < bytes; i += int64_t(gridDim.x) * 256) p[i] = 0;
 }
 
+// Whether an operand's stored rows are whole 16-byte vectors.
+bool on_grid(int dtype, bool by_k, const void* p, int64_t ld, int64_t rows, int64_t k) {
+  const int64_t v = dtype == CCL_BF16 ? 8 : 4;
+  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % v == 0 && (by_k ? rows : k) % v == 0;
+}
+
 }  // namespace
 }  // namespace prod
 
@@ -210,6 +216,10 @@ int launch_slope(int dtype, const SlopeArgs& args, void* stream, std::string* er
 int launch_product(int dtype, bool a_by_k, bool b_by_k, ProductMode mode, const ProductArgs& args, void* stream,
                    std::string* err) {
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  if (prod::on_grid(dtype, a_by_k, args.a, args.lda, args.m, args.k) &&
+      prod::on_grid(dtype, b_by_k, args.b, args.ldb, args.n, args.k))
+    return dtype == CCL_BF16 ? prod::launch_tile_bf16(a_by_k, b_by_k, mode, args, s, err)
+                             : prod::launch_tile_f32(a_by_k, b_by_k, mode, args, s, err);
   return dtype == CCL_BF16 ? prod::launch_any<prod::bf16>(a_by_k, b_by_k, mode, args, s, err)
                            : prod::launch_any<float>(a_by_k, b_by_k, mode, args, s, err);
 }

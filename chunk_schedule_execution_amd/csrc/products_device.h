@@ -23,32 +23,58 @@ __device__ inline T narrow(float v) {
   return T(v);  // nearest-even
 }
 
+// exp(-v) and 1 / v by the hardware's own instructions (one fp32 step each).
+__device__ inline float exp_of_minus(float v) { return __builtin_amdgcn_exp2f(v * -1.44269504088896341f); }
+__device__ inline float reciprocal(float v) { return __builtin_amdgcn_rcpf(v); }
+
+// 1 - erf(x) for x >= 0 by the rational approximation 7.1.26 of Abramowitz and Stegun's
+// handbook: off by at most 1.5e-7, about one step of fp32 at 1. e: exp(-x^2).
+__device__ inline float erfc_of(float x, float e) {
+  const float t = reciprocal(1.0f + 0.3275911f * x);
+  return e * t *
+         (0.254829592f + t * (-0.284496736f + t * (1.421413741f + t * (-1.453152027f + t * 1.061405429f))));
+}
+
+// (1 + tanh(u)) / 2 = 1 / (1 + exp(-2 u)), so gelu_tanh and silu are both z / (1 + exp(-v)).
+__device__ inline float gelu_tanh_arg(float z) { return 1.59576912160573071f * (z + 0.044715f * z * z * z); }
+
 __device__ inline float act_value(float z, int act) {
   switch (act) {
     case CCL_ACT_RELU: return z < 0.0f ? 0.0f : z;
-    case CCL_ACT_GELU: return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
-    case CCL_ACT_GELU_TANH: return 0.5f * z * (1.0f + tanhf(0.79788456080286536f * (z + 0.044715f * z * z * z)));
-    case CCL_ACT_SILU: return z / (1.0f + expf(-z));
+    case CCL_ACT_GELU: {
+      const float x = fabsf(z) * 0.70710678118654752f;
+      const float half = 0.5f * erfc_of(x, exp_of_minus(x * x));
+      return z * (z < 0.0f ? half : 1.0f - half);
+    }
+    case CCL_ACT_GELU_TANH: return z * reciprocal(1.0f + exp_of_minus(gelu_tanh_arg(z)));
+    case CCL_ACT_SILU: return z * reciprocal(1.0f + exp_of_minus(z));
   }
   return z;
 }
 
 __device__ inline float act_slope(float z, int act) {
   switch (act) {
-    case CCL_ACT_RELU: return z > 0.0f ? 1.0f : (z <= 0.0f ? 0.0f : z);
-    case CCL_ACT_GELU:
-      return 0.5f * (1.0f + erff(z * 0.70710678118654752f)) + z * expf(-0.5f * z * z) * 0.39894228040143268f;
-    case CCL_ACT_GELU_TANH: {
-      const float t = tanhf(0.79788456080286536f * (z + 0.044715f * z * z * z));
-      return 0.5f * (1.0f + t) + 0.5f * z * (1.0f - t * t) * 0.79788456080286536f * (1.0f + 0.134145f * z * z);
+    case CCL_ACT_RELU: return z > 0.0f ? 1.0f : 0.0f;
+    case CCL_ACT_GELU: {
+      const float x = fabsf(z) * 0.70710678118654752f;
+      const float e = exp_of_minus(x * x);
+      const float half = 0.5f * erfc_of(x, e);
+      return (z < 0.0f ? half : 1.0f - half) + z * e * 0.39894228040143268f;
     }
+    case CCL_ACT_GELU_TANH:
     case CCL_ACT_SILU: {
-      const float p = 1.0f / (1.0f + expf(-z));
-      return p * (1.0f + z * (1.0f - p));
+      // p = 1 / (1 + exp(-v)): p + z p (1 - p) v'; 1 - p without cancellation
+      const float v = act == CCL_ACT_SILU ? z : gelu_tanh_arg(z);
+      const float dv = act == CCL_ACT_SILU ? 1.0f : 1.59576912160573071f * (1.0f + 0.134145f * z * z);
+      const float e = exp_of_minus(v), p = reciprocal(1.0f + e);
+      return p + z * p * (v > 0.0f ? e * p : 1.0f - p) * dv;
     }
   }
   return 1.0f;
 }
+
+// A value that all lanes share, for the compiler to keep in scalar registers.
+__device__ inline int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
 // One tile of rows of a group.
 struct RowTile {
@@ -98,12 +124,12 @@ __device__ inline RowTile find_tile(const int32_t* offsets, int groups, int64_t 
     const unsigned long long hit = __ballot(tile < upto);
     if (hit) {
       const int l = __ffsll(hit) - 1;
-      const int first = __shfl(upto - tiles, l);
-      const int64_t row = int64_t(__shfl(lo, l)) + int64_t(tile - first) * height;
-      return {base + l, tile, row, int64_t(__shfl(hi, l))};
+      const int first = __builtin_amdgcn_readlane(upto - tiles, l);
+      const int64_t row = int64_t(__builtin_amdgcn_readlane(lo, l)) + int64_t(tile - first) * height;
+      return {base + l, tile, row, int64_t(__builtin_amdgcn_readlane(hi, l))};
     }
-    carry_tiles = __shfl(upto, 63);
-    carry_max = __shfl(hi, 63);
+    carry_tiles = __builtin_amdgcn_readlane(upto, 63);
+    carry_max = __builtin_amdgcn_readlane(hi, 63);
   }
   return {-1, tile, 0, 0};
 }
@@ -120,6 +146,7 @@ __device__ inline void group_bounds(const int32_t* offsets, int64_t rows, int gr
   for (int e = 1 + lane; e <= group; e += 64) top = max(top, min(offsets[e], int(rows)));
 #pragma unroll
   for (int d = 32; d >= 1; d >>= 1) top = max(top, __shfl_xor(top, d));
+  top = uniform(top);
   lo = top;
   hi = max(top, min(offsets[group + 1], int(rows)));
 }
