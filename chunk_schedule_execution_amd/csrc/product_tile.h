@@ -71,20 +71,20 @@ struct OperandTile {
 
   static __device__ inline int swizzle(int k) { return kSize == 2 ? (k & 3) << 1 : ((k >> 2) & 3) << 2; }
 
-  // Starts the loads of the step whose `left` summed values (>= 1) remain, into `lds`, and
-  // moves on to the next step. Out of range reads give zeros.
+  // Starts the loads of the step whose `left` summed values remain, into `lds`, and moves
+  // on to the next step. Reads out of range (all of them when none remain) give zeros.
   __device__ inline void load(T* lds, int64_t left) {
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    unsigned to = unsigned((uintptr_t)(lds_ptr)lds) + wave * 1024;
+    asm volatile("" : "+s"(to));
     const int64_t rest = ByK ? (min(int64_t(kStep), left) - 1) * ld_bytes + records : records;
     const __amdgpu_buffer_rsrc_t rsrc =
-        __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base), 0, int(rest), 0x00020000);
+        __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base), 0, left > 0 ? int(rest) : 0, 0x00020000);
     // by rows, the last step: chunks behind the row's end would be the next row's values
     const bool out = !ByK && left < kStep && kc >= left;
 #pragma unroll
     for (int i = 0; i < kLoads; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          rsrc, (lds_ptr)(reinterpret_cast<char*>(lds) + (i * Threads + wave * 64) * 16), 16, out ? -1 : voff[i], 0, 0,
-          0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_ptr)(uintptr_t)(to + i * Threads * 16), 16, out ? -1 : voff[i], 0, 0, 0);
     base += step_bytes;
     if (!ByK) records -= 128;
   }
@@ -205,15 +205,33 @@ __device__ inline void act8(float* v, int act) {
 #undef CCL_ACT8
 }
 
+// Every wave's loads into LDS but its latest Left have arrived, and every wave's reads
+// before this point are done.
+template <int Left>
 __device__ inline void steps_arrived() {
-  __builtin_amdgcn_s_waitcnt(0x0F70);  // all of this wave's loads into LDS
+  __builtin_amdgcn_s_waitcnt(0x0F70 | (Left & 15) | (Left >> 4) << 14);  // vmcnt
   __syncthreads();
+}
+
+// Which tile a workgroup computes. Workgroups go round the 8 XCDs, each with an L2 of its
+// own, so XCD x takes the x-th eighth of the tiles; within it 8 bands (rows of tiles) are
+// walked together, column by column, so that the 32 workgroups that run there at a time
+// share 8 row and 4 column tiles. 16384 x 16384 x 4096 gradient of x: 1958 -> 1.7 ms.
+__device__ inline void place_tile(unsigned id, unsigned tiles, int tiles_n, int& band, int& column) {
+  constexpr unsigned kXcds = 8;
+  constexpr int kBands = 8;
+  const unsigned x = id % kXcds, whole = tiles / kXcds, rest = tiles % kXcds;
+  const int l = int(x * whole + min(x, rest) + id / kXcds);
+  // quotients are computed in vector registers: uniform() brings them back
+  const int slab = uniform(l / (kBands * tiles_n)), in = l - slab * kBands * tiles_n;
+  const int bands = min(kBands, int(tiles) / tiles_n - slab * kBands);
+  column = uniform(in / bands);
+  band = slab * kBands + in - column * bands;
 }
 
 // ---- the kernel ---------------------------------------------------------------------------
 // BM x BN values per workgroup, WM x WN waves, each (BM / WM) x (BN / WN) by matrix
-// instructions of 16 x 16. Two LDS buffers: the loads of a step run while the step before
-// is multiplied; one barrier per step orders both directions.
+// instructions of 16 x 16. Two LDS buffers, one barrier per step.
 template <typename T, bool AByK, bool BByK, int BM, int BN, int WM, int WN>
 __device__ inline void product_tile(const ProductArgs& g, ProductMode mode, int tiles_m, int tiles_n) {
   constexpr int Threads = WM * WN * 64, FM = BM / WM / 16, FN = BN / WN / 16;
@@ -228,10 +246,9 @@ __device__ inline void product_tile(const ProductArgs& g, ProductMode mode, int 
   const T* A = static_cast<const T*>(g.a);
   const T* B = static_cast<const T*>(g.b);
   T* C = static_cast<T*>(g.c);
-  // quotients are computed in vector registers: uniform() brings them back
-  const int tile = blockIdx.x;
-  const int band = uniform(tile / tiles_n);
-  const int64_t col = int64_t(tile - band * tiles_n) * BN;
+  int band, column;
+  place_tile(blockIdx.x, gridDim.x, tiles_n, band, column);
+  const int64_t col = int64_t(column) * BN;
   int group = 0;
   int64_t row = 0, m_end = g.m, k_lo = 0, k_hi = g.k;
   if (mode == kRaggedK) {
@@ -265,48 +282,72 @@ __device__ inline void product_tile(const ProductArgs& g, ProductMode mode, int 
     FragmentReader<T, BByK, BN, FN> rb;
     ra.init(wm);
     rb.init(wn);
-    auto compute = [&](const T* la, const T* lb) {
+    // A step is 2 FM rows of fragments (both halves), multiplied one after another. Reads
+    // run Ahead rows ahead: a buffer's last read is done that many rows before its last
+    // products, and there the step's only barrier stands. Behind it the next buffer is
+    // read and the loads of the step after next may overwrite this one, with a whole step
+    // to arrive; the rows still to be multiplied cover the barrier and the first reads.
+    // Loads behind the end give zeros and nothing multiplies them, so no step branches.
+    typedef decltype(ra.read(a0, 0, 0)) vec;
+    constexpr int Rows = 2 * FM, Ahead = 4, Ring = 8;
+    static_assert(Ahead <= FM && Rows % Ring == 0, "a ring of fragments");
+    vec fa[Ring], fb[2][FN];
+    auto read_a = [&](const T* la, int r) { fa[r % Ring] = ra.read(la, r % FM, r / FM % 2); };
+    auto read_b = [&](const T* lb, int h) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        decltype(rb.read(lb, 0, 0)) fb[FN];
-#pragma unroll
-        for (int j = 0; j < FN; ++j) fb[j] = rb.read(lb, j, h);
-#pragma unroll
-        for (int i = 0; i < FM; ++i) {
-          const auto fa = ra.read(la, i, h);
-#pragma unroll
-          for (int j = 0; j < FN; ++j) acc[i][j] = multiply(fb[j], fa, acc[i][j]);
-        }
-      }
+      for (int j = 0; j < FN; ++j) fb[h][j] = rb.read(lb, j, h);
     };
-    int64_t left = k_hi - k_lo;
+    auto products = [&](int r) {
+#pragma unroll
+      for (int j = 0; j < FN; ++j) acc[r % FM][j] = multiply(fb[r / FM][j], fa[r % Ring], acc[r % FM][j]);
+    };
+    int64_t left = k_hi - k_lo;  // of the step being multiplied
     ta.load(a0, left);
     tb.load(b0, left);
-    for (; left > 0; left -= 2 * kStep) {
-      steps_arrived();
-      if (left > kStep) {
-        ta.load(a1, left - kStep);
-        tb.load(b1, left - kStep);
+    ta.load(a1, left - kStep);
+    tb.load(b1, left - kStep);
+    steps_arrived<decltype(ta)::kLoads + decltype(tb)::kLoads>();
+    read_b(b0, 0);
+#pragma unroll
+    for (int r = 0; r < Ahead; ++r) read_a(a0, r);
+    auto step = [&](T* la, T* lb, const T* na, const T* nb) {
+      // the scheduling barriers keep reads from sinking back to their uses
+#pragma unroll
+      for (int r = 0; r < Rows - Ahead; ++r) {
+        if (r == FM - Ahead) read_b(lb, 1);
+        read_a(la, r + Ahead);
+        products(r);
+        __builtin_amdgcn_sched_barrier(0);
       }
-      compute(a0, b0);
-      if (left <= kStep) break;
-      steps_arrived();
-      if (left > 2 * kStep) {
-        ta.load(a0, left - 2 * kStep);
-        tb.load(b0, left - 2 * kStep);
+      steps_arrived<0>();
+      read_b(nb, 0);
+#pragma unroll
+      for (int r = 0; r < Ahead; ++r) {
+        read_a(na, r);
+        products(Rows - Ahead + r);
+        if (r == 0) ta.load(la, left - 2 * kStep);
+        if (r == 1) tb.load(lb, left - 2 * kStep);
+        __builtin_amdgcn_sched_barrier(0);
       }
-      compute(a1, b1);
+      left -= kStep;
+    };
+    while (true) {
+      step(a0, b0, a1, b1);
+      if (left <= 0) break;
+      step(a1, b1, a0, b0);
+      if (left <= 0) break;
     }
+    __builtin_amdgcn_s_waitcnt(0x0F70);  // the loads behind the end, before LDS is used again
     __syncthreads();
   }
 
-  // Results go through LDS, a wave's 16 (or 8) KiB at a time and to itself alone, so that
+  // Results go through LDS, a wave's 16 rows at a time and to itself alone, so that
   // rows are read and written in 16-byte vectors and the epilogue's code exists once.
   constexpr int WTN = BN / WN, kChunks = WTN / 4;        // 16-byte chunks of fp32 per row
   constexpr int kLanesPerRow = WTN / 8, kRowsPerPass = 64 / kLanesPerRow;
-  constexpr int kStage = 2;                              // fragments of rows per stage
-  float* const stage = reinterpret_cast<float*>(wave < WM * WN / 2 ? a0 : a1) + (wave % (WM * WN / 2)) * (kStage * 16 * WTN);
-  static_assert(kStage * 16 * WTN * 4 * (WM * WN / 2) <= BM * 128, "a wave's stage fits");
+  constexpr int kStage = 1;                              // fragments of rows per stage
+  float* const stage = reinterpret_cast<float*>(a0) + wave * (kStage * 16 * WTN);
+  static_assert(kStage * 16 * WTN * 4 * WM * WN <= BM * 128, "the waves' stages fit");
   const T* bias = g.bias && !nothing ? static_cast<const T*>(g.bias) + group * g.bias_stride : nullptr;
   const T* residual = static_cast<const T*>(g.residual);
   T* preact = static_cast<T*>(g.preact);
