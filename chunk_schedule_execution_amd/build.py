@@ -21,7 +21,7 @@ BUILD = os.path.join(ROOT, "_build")
 
 HOST_SOURCES = ["compiler.cpp", "simulate.cpp", "capi.cpp", "tune.cpp", "specialize.cpp", "products.cpp"]
 DEVICE_SOURCES = ["executor.hip", "static_scratch.hip", "hop_probe.hip", "products.hip", "product_tile_bf16.hip",
-                  "product_tile_f32.hip", "exchange.hip"]
+                  "product_tile_f32.hip", "product_rows.hip", "exchange.hip"]
 ARCH = "gfx950"
 COMMON = ["-O3", "-std=c++17", "-fPIC", "-Wall", "-Wno-unused-result", "-I", os.path.join(ROOT, "include"), "-I", "/opt/rocm/include"]
 DEVICE_FLAGS = [f"--offload-arch={ARCH}", "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",

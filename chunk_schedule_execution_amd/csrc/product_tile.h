@@ -42,15 +42,15 @@ struct OperandTile {
   int voff[kLoads];
   int kc;  // by rows: first k value of this lane's chunk
 
-  // row: first row (or column) of the tile, end: one past the last readable one; k_lo, k_hi:
-  // the summed range.
+  // row: first row (or column) of the tile, end: one past the last; k_lo, k_hi: the summed
+  // range. The vector around the last value is read whole.
   __device__ inline void init(const T* p, int64_t ld, int64_t row, int64_t end, int64_t k_lo, int64_t k_hi) {
     const int tid = threadIdx.x;
     ld_bytes = ld * kSize;
     if constexpr (ByK) {
       base = reinterpret_cast<const char*>(p + k_lo * ld + row);
       step_bytes = ld_bytes * kStep;
-      records = (end - row) * kSize;  // of the last row
+      records = (end - row + kVec - 1) / kVec * 16;  // of the last row: whole vectors
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
         const int q = i * Threads + tid, k = q / kChunks, c = (q % kChunks) ^ swizzle(k);
@@ -59,7 +59,7 @@ struct OperandTile {
     } else {
       base = reinterpret_cast<const char*>(p + row * ld + k_lo);
       step_bytes = 128;
-      records = (min(int64_t(R), end - row) - 1) * ld_bytes + (k_hi - k_lo) * kSize;
+      records = (min(int64_t(R), end - row) - 1) * ld_bytes + (k_hi - k_lo + kVec - 1) / kVec * 16;
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
         const int q = i * Threads + tid, r = q / 8, c = (q % 8) ^ (r & 7);
@@ -152,59 +152,6 @@ __device__ inline f32x4 multiply(f32x4 x, f32x4 y, f32x4 acc) {
   return acc;
 }
 
-// ---- results -----------------------------------------------------------------------------
-// 8 neighbouring values of a row; `vec`: the row lies on the 16-byte grid; `n`: how many of
-// them exist.
-template <typename T>
-__device__ inline void load8(const T* p, bool vec, int n, float* v) {
-  if (vec && n >= 8) {
-    constexpr int V = 16 / int(sizeof(T));
-    typedef T pack __attribute__((ext_vector_type(V)));
-#pragma unroll
-    for (int h = 0; h < 8 / V; ++h) {
-      const pack x = reinterpret_cast<const pack*>(p)[h];
-#pragma unroll
-      for (int q = 0; q < V; ++q) v[h * V + q] = widen(x[q]);
-    }
-  } else {
-#pragma unroll
-    for (int q = 0; q < 8; ++q) v[q] = q < n ? widen(p[q]) : 0.0f;
-  }
-}
-template <typename T>
-__device__ inline void store8(T* p, bool vec, int n, const float* v) {
-  if (vec && n >= 8) {
-    constexpr int V = 16 / int(sizeof(T));
-    typedef T pack __attribute__((ext_vector_type(V)));
-#pragma unroll
-    for (int h = 0; h < 8 / V; ++h) {
-      pack x;
-#pragma unroll
-      for (int q = 0; q < V; ++q) x[q] = narrow<T>(v[h * V + q]);
-      reinterpret_cast<pack*>(p)[h] = x;
-    }
-  } else {
-#pragma unroll
-    for (int q = 0; q < 8; ++q)
-      if (q < n) p[q] = narrow<T>(v[q]);
-  }
-}
-// The activation of 8 values: the branch is taken once for them.
-__device__ inline void act8(float* v, int act) {
-#define CCL_ACT8(A)                                            \
-  case A:                                                      \
-    _Pragma("unroll") for (int q = 0; q < 8; ++q) v[q] = act_value(v[q], A); \
-    break;
-  switch (act) {
-    CCL_ACT8(CCL_ACT_RELU)
-    CCL_ACT8(CCL_ACT_GELU)
-    CCL_ACT8(CCL_ACT_GELU_TANH)
-    CCL_ACT8(CCL_ACT_SILU)
-    default: break;
-  }
-#undef CCL_ACT8
-}
-
 // Every wave's loads into LDS but its latest Left have arrived, and every wave's reads
 // before this point are done.
 template <int Left>
@@ -216,7 +163,7 @@ __device__ inline void steps_arrived() {
 // Which tile a workgroup computes. Workgroups go round the 8 XCDs, each with an L2 of its
 // own, so XCD x takes the x-th eighth of the tiles; within it 8 bands (rows of tiles) are
 // walked together, column by column, so that the 32 workgroups that run there at a time
-// share 8 row and 4 column tiles. 16384 x 16384 x 4096 gradient of x: 1958 -> 1.7 ms.
+// share 8 row and 4 column tiles: 8192^3 795 us, and 821 us in the order of the columns.
 __device__ inline void place_tile(unsigned id, unsigned tiles, int tiles_n, int& band, int& column) {
   constexpr unsigned kXcds = 8;
   constexpr int kBands = 8;
@@ -270,6 +217,12 @@ __device__ inline void product_tile(const ProductArgs& g, ProductMode mode, int 
   m_end = uniform(int(m_end));
   k_lo = uniform(int(k_lo));
   k_hi = uniform(int(k_hi));
+  if (gridDim.y > 1) {  // this workgroup's share of the summed dimension, in whole steps
+    const int steps = int((k_hi - k_lo + kStep - 1) / kStep);
+    const int64_t lo = k_lo + int64_t(steps) * blockIdx.y / gridDim.y * kStep;
+    k_hi = min(k_hi, k_lo + int64_t(steps) * (blockIdx.y + 1) / gridDim.y * kStep);
+    k_lo = lo;
+  }
 
   f32x4 acc[FM][FN] = {};
   const int wm = wave / WN * (BM / WM), wn = wave % WN * (BN / WN);
@@ -377,6 +330,10 @@ __device__ inline void product_tile(const ProductArgs& g, ProductMode mode, int 
       *reinterpret_cast<f32x4*>(v) = *reinterpret_cast<const f32x4*>(stage + r * WTN + ((chunk ^ r) % kChunks) * 4);
       *reinterpret_cast<f32x4*>(v + 4) =
           *reinterpret_cast<const f32x4*>(stage + r * WTN + (((chunk + 1) ^ r) % kChunks) * 4);
+      if (g.partial) {
+        store8(g.partial + (int64_t(blockIdx.y) * g.m + at) * g.n + c, g.n % 4 == 0, n, v);
+        continue;
+      }
 #pragma unroll
       for (int q = 0; q < 8; ++q) v[q] += bv[q];
       if (preact) store8(preact + at * g.ldp + c, vec_p, n, v);
@@ -401,17 +358,18 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void product_tile_kernel(ProductArg
 }
 
 template <typename T, int BM, int BN, int WM, int WN>
-int launch_tile(bool a_by_k, bool b_by_k, ProductMode mode, const ProductArgs& g, hipStream_t s, std::string* err) {
+int launch_tile(bool a_by_k, bool b_by_k, ProductMode mode, const ProductArgs& g, int splits, hipStream_t s,
+                std::string* err) {
   const int64_t tiles_n = (g.n + BN - 1) / BN, tiles_m = (g.m + BM - 1) / BM;
   const int64_t grid = mode == kRaggedK ? g.groups * tiles_m * tiles_n
                        : mode == kRaggedM ? (tiles_m + g.groups) * tiles_n : tiles_m * tiles_n;
-  if (grid > 0x7fffffff) {
-    *err = "product: more than 2^31 tiles";
+  if (grid > 0x7fffff) {  // a grid holds less than 2^32 threads
+    *err = "product: more than 2^23 tiles";
     return CCL_ERR_INVALID_ARGUMENT;
   }
   if (grid == 0) return CCL_OK;
   auto go = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, dim3(unsigned(grid)), dim3(WM * WN * 64), 0, s, g, mode, int(tiles_m), int(tiles_n));
+    hipLaunchKernelGGL(kernel, dim3(unsigned(grid), splits), dim3(WM * WN * 64), 0, s, g, mode, int(tiles_m), int(tiles_n));
   };
   if (a_by_k && b_by_k) go(product_tile_kernel<T, true, true, BM, BN, WM, WN>);
   else if (b_by_k) go(product_tile_kernel<T, false, true, BM, BN, WM, WN>);
@@ -423,10 +381,6 @@ int launch_tile(bool a_by_k, bool b_by_k, ProductMode mode, const ProductArgs& g
 }
 
 }  // namespace
-
-// Defined with their kernels in product_tile_bf16.hip and product_tile_f32.hip.
-int launch_tile_bf16(bool a_by_k, bool b_by_k, ProductMode mode, const ProductArgs& g, hipStream_t s, std::string* err);
-int launch_tile_f32(bool a_by_k, bool b_by_k, ProductMode mode, const ProductArgs& g, hipStream_t s, std::string* err);
 
 }  // namespace prod
 }  // namespace ccl

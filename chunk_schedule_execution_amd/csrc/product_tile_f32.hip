@@ -4,9 +4,9 @@
 namespace ccl {
 namespace prod {
 
-int launch_tile_f32(bool a_by_k, bool b_by_k, ProductMode mode, const ProductArgs& g, hipStream_t s,
-                    std::string* err) {
-  return launch_tile<float, 128, 128, 2, 2>(a_by_k, b_by_k, mode, g, s, err);
+int launch_tile_f32(bool a_by_k, bool b_by_k, ProductMode mode, const ProductArgs& g, const ProductPlan& plan,
+                    hipStream_t s, std::string* err) {
+  return launch_tile<float, 128, 128, 2, 2>(a_by_k, b_by_k, mode, g, plan.splits, s, err);
 }
 
 }  // namespace prod

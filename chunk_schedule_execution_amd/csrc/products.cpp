@@ -61,21 +61,78 @@ void aligned(const ccl_linear_desc& d, const void* p, const char* name) {
 
 int64_t align16(int64_t bytes) { return (bytes + 15) / 16 * 16; }
 
-// Workspace of a backward call: dz, then the partial sums of the bias gradient.
-struct BackwardSpace {
-  int64_t dz = 0, partial = 0, total = 0, ld_dz = 0;
+// The products of a call, without pointers where only sizes are asked for.
+ProductArgs forward_args(const ccl_linear_desc& d) {
+  ProductArgs g;
+  g.lda = d.ld_x;
+  g.ldb = d.ld_w;
+  g.ldc = d.ld_out;
+  g.m = d.rows;
+  g.n = d.out_features;
+  g.k = d.in_features;
+  g.groups = d.experts;
+  g.b_stride = d.out_features * d.ld_w;
+  g.bias_stride = d.out_features;
+  g.ldr = d.ld_residual;
+  g.ldp = d.ld_preact;
+  g.act = d.activation;
+  return g;
+}
+// dx = dz w: the summed dimension is out_features, along w's rows.
+ProductArgs dx_args(const ccl_linear_desc& d, int64_t ld_dz) {
+  ProductArgs g;
+  g.lda = ld_dz;
+  g.ldb = d.ld_w;
+  g.ldc = d.ld_dx;
+  g.m = d.rows;
+  g.n = d.in_features;
+  g.k = d.out_features;
+  g.groups = d.experts;
+  g.b_stride = d.out_features * d.ld_w;
+  return g;
+}
+// dw = dz^T x: the summed dimension is the rows.
+ProductArgs dw_args(const ccl_linear_desc& d, int64_t ld_dz) {
+  ProductArgs g;
+  g.lda = ld_dz;
+  g.ldb = d.ld_x;
+  g.ldc = d.ld_dw;
+  g.m = d.out_features;
+  g.n = d.in_features;
+  g.k = d.rows;
+  g.groups = d.experts;
+  g.c_stride = d.out_features * d.ld_dw;
+  return g;
+}
+OperandGrid grid_of(const ccl_linear_desc& d) { return d.flags & CCL_LINEAR_UNALIGNED ? kOffGrid : kByStrides; }
+
+// Workspace of a backward call: dz, the partial sums of the bias gradient, and what the
+// two products need, one after the other.
+struct BackwardPlan {
+  bool own_dz = false;  // dz is written: there is an activation, or dout lies off the 16-byte grid
+  int64_t ld_dz = 0, at_partial = 0, at_product = 0, total = 0;
+  ProductPlan dx, dw;
 };
-BackwardSpace backward_space(const ccl_linear_desc& d, bool grouped) {
-  BackwardSpace s;
+BackwardPlan backward_plan(const ccl_linear_desc& d, bool grouped) {
+  BackwardPlan s;
   const int size = elem_size(d.dtype);
-  s.ld_dz = align16(d.out_features * size) / size;
-  s.partial = d.activation == CCL_ACT_NONE ? 0 : align16(d.rows * s.ld_dz * size);
-  s.total = s.partial + align16(slope_tiles(d.rows, grouped ? d.experts : 0) * d.out_features * 4);
+  const int64_t padded = align16(d.out_features * size) / size;
+  s.own_dz = d.activation != CCL_ACT_NONE || grid_of(d) == kOffGrid || d.ld_out * size % 16 || padded != d.out_features;
+  s.ld_dz = s.own_dz ? padded : d.ld_out;
+  s.at_partial = s.own_dz ? align16(d.rows * padded * size) : 0;
+  s.at_product = s.at_partial + align16(slope_tiles(d.rows, grouped ? d.experts : 0) * d.out_features * 4);
+  const OperandGrid dz = s.own_dz ? kPadded : kByStrides;
+  s.dx = plan_product(d.dtype, false, true, grouped ? kRaggedM : kPlain, dx_args(d, s.ld_dz), dz, grid_of(d));
+  s.dw = plan_product(d.dtype, true, true, grouped ? kRaggedK : kPlain, dw_args(d, s.ld_dz), dz, grid_of(d));
+  s.total = s.at_product + std::max(s.dx.bytes, s.dw.bytes);
   return s;
+}
+ProductPlan forward_plan(const ccl_linear_desc& d, bool grouped) {
+  return plan_product(d.dtype, false, false, grouped ? kRaggedM : kPlain, forward_args(d), grid_of(d), grid_of(d));
 }
 
 int64_t workspace_bytes_of(const ccl_linear_desc& d, bool grouped, bool backward) {
-  return backward ? backward_space(d, grouped).total : 0;
+  return backward ? backward_plan(d, grouped).total : forward_plan(d, grouped).bytes;
 }
 
 void check_workspace(const void* ws, size_t have, int64_t need) {
@@ -102,29 +159,18 @@ int forward(const ccl_linear_desc* desc, bool grouped, const int32_t* offsets, c
   aligned(d, residual, "residual");
   aligned(d, out, "out");
   aligned(d, preact, "preact");
-  check_workspace(ws, ws_bytes, workspace_bytes_of(d, grouped, false));
-  ProductArgs g;
+  const ProductPlan plan = forward_plan(d, grouped);
+  check_workspace(ws, ws_bytes, plan.bytes);
+  ProductArgs g = forward_args(d);
   g.a = x;
   g.b = w;
   g.c = out;
-  g.lda = d.ld_x;
-  g.ldb = d.ld_w;
-  g.ldc = d.ld_out;
-  g.m = d.rows;
-  g.n = d.out_features;
-  g.k = d.in_features;
   g.offsets = offsets;
-  g.groups = d.experts;
-  g.b_stride = d.out_features * d.ld_w;
   g.bias = bias;
-  g.bias_stride = d.out_features;
   g.residual = residual;
-  g.ldr = d.ld_residual;
   g.preact = preact;
-  g.ldp = d.ld_preact;
-  g.act = d.activation;
   std::string err;
-  launched(launch_product(d.dtype, false, false, grouped ? kRaggedM : kPlain, g, stream, &err), err);
+  launched(launch_product(d.dtype, false, false, grouped ? kRaggedM : kPlain, g, plan, ws, stream, &err), err);
   return CCL_OK;
 }
 
@@ -147,12 +193,10 @@ int backward(const ccl_linear_desc* desc, bool grouped, const int32_t* offsets, 
   aligned(d, dx, "dx");
   aligned(d, dw, "dw");
   aligned(d, dbias, "dbias");
-  check_workspace(ws, ws_bytes, workspace_bytes_of(d, grouped, true));
-  const BackwardSpace space = backward_space(d, grouped);
+  const BackwardPlan plan = backward_plan(d, grouped);
+  check_workspace(ws, ws_bytes, plan.total);
+  unsigned char* const space = static_cast<unsigned char*>(ws);
   std::string err;
-  // dz: dout itself without an activation
-  const void* dz = dout;
-  int64_t ld_dz = d.ld_out;
   SlopeArgs sl;
   sl.dout = dout;
   sl.preact = preact;
@@ -164,45 +208,30 @@ int backward(const ccl_linear_desc* desc, bool grouped, const int32_t* offsets, 
   sl.groups = d.experts;
   sl.act = d.activation;
   sl.dbias = dbias;
-  sl.partial = reinterpret_cast<float*>(static_cast<unsigned char*>(ws) + space.partial);
-  if (d.activation != CCL_ACT_NONE && (dx || dw)) {
-    sl.dz = static_cast<unsigned char*>(ws) + space.dz;
-    sl.ldz = space.ld_dz;
-    dz = sl.dz;
-    ld_dz = space.ld_dz;
+  sl.partial = reinterpret_cast<float*>(space + plan.at_partial);
+  if (plan.own_dz && (dx || dw)) {
+    sl.dz = space;
+    sl.ldz = plan.ld_dz;
   }
   launched(launch_slope(d.dtype, sl, stream, &err), err);
+  const void* dz = plan.own_dz ? space : dout;
   if (dx && d.rows > 0) {
-    ProductArgs g;  // dx = dz w: the summed dimension is out_features, along w's rows
+    ProductArgs g = dx_args(d, plan.ld_dz);
     g.a = dz;
     g.b = w;
     g.c = dx;
-    g.lda = ld_dz;
-    g.ldb = d.ld_w;
-    g.ldc = d.ld_dx;
-    g.m = d.rows;
-    g.n = d.in_features;
-    g.k = d.out_features;
     g.offsets = offsets;
-    g.groups = d.experts;
-    g.b_stride = d.out_features * d.ld_w;
-    launched(launch_product(d.dtype, false, true, grouped ? kRaggedM : kPlain, g, stream, &err), err);
+    launched(launch_product(d.dtype, false, true, grouped ? kRaggedM : kPlain, g, plan.dx, space + plan.at_product, stream, &err),
+             err);
   }
   if (dw) {
-    ProductArgs g;  // dw = dz^T x: the summed dimension is the rows
+    ProductArgs g = dw_args(d, plan.ld_dz);
     g.a = dz;
     g.b = x;
     g.c = dw;
-    g.lda = ld_dz;
-    g.ldb = d.ld_x;
-    g.ldc = d.ld_dw;
-    g.m = d.out_features;
-    g.n = d.in_features;
-    g.k = d.rows;
     g.offsets = offsets;
-    g.groups = d.experts;
-    g.c_stride = d.out_features * d.ld_dw;
-    launched(launch_product(d.dtype, true, true, kRaggedK, g, stream, &err), err);
+    launched(launch_product(d.dtype, true, true, grouped ? kRaggedK : kPlain, g, plan.dw, space + plan.at_product, stream, &err),
+             err);
   }
   return CCL_OK;
 }

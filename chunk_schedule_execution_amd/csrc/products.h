@@ -31,13 +31,30 @@ struct ProductArgs {
   void* preact = nullptr;
   int64_t ldr = 0, ldp = 0;
   int act = 0;
+  float* partial = nullptr;  // set: the splits' fp32 sums go here, [split][m][n], and nothing else happens
 };
 
-int launch_product(int dtype, bool a_by_k, bool b_by_k, ProductMode mode, const ProductArgs& args, void* stream,
-                   std::string* err);
+// How a product is run, from its sizes alone.
+enum ProductKind : int { kRows16, kRows32, kRows64, kTile128, kTile256 };
+struct ProductPlan {
+  ProductKind kind = kTile128;
+  int columns = 1;                   // few-row kinds: 16-column fragments per workgroup
+  int splits = 1;                    // of the summed dimension
+  bool vec = true;                   // few-row kinds: both operands lie on the 16-byte grid
+  bool copy_a = false, copy_b = false;  // tiles: operands that are first copied onto that grid
+  int64_t ld_a = 0, ld_b = 0;        // of the copies
+  int64_t at_a = 0, at_b = 0, at_partial = 0, bytes = 0;  // workspace layout
+};
+// Where an operand's stored rows lie: on the 16-byte grid if strides and lengths are whole
+// vectors; off it, its base pointer being unaligned; or on it with zeros up to the vector.
+enum OperandGrid : int { kByStrides, kOffGrid, kPadded };
+ProductPlan plan_product(int dtype, bool a_by_k, bool b_by_k, ProductMode mode, const ProductArgs& args,
+                         OperandGrid a_grid, OperandGrid b_grid);
+int launch_product(int dtype, bool a_by_k, bool b_by_k, ProductMode mode, const ProductArgs& args,
+                   const ProductPlan& plan, void* workspace, void* stream, std::string* err);
 
-// dz = dout act'(preact) (skipped when dz is NULL) and its column sums by group (skipped
-// when dbias is NULL). partial: fp32, slope_tiles() x n.
+// dz = dout act'(preact) (skipped when dz is NULL; zeros behind a row up to ldz) and its
+// column sums by group (skipped when dbias is NULL). partial: fp32, slope_tiles() x n.
 struct SlopeArgs {
   const void* dout = nullptr;
   const void* preact = nullptr;
@@ -50,10 +67,8 @@ struct SlopeArgs {
   int groups = 1;
   int act = 0;
 };
-int64_t slope_tiles(int64_t rows, int groups);
+int64_t slope_tiles(int64_t rows, int groups);  // groups: 0 without offsets
 int launch_slope(int dtype, const SlopeArgs& args, void* stream, std::string* err);
-
-int launch_fill_zero(void* p, int64_t bytes, void* stream, std::string* err);
 
 int64_t route_workspace(int64_t slots, int experts);
 int launch_route(const int32_t* ids, int64_t slots, int experts, int32_t* offsets, int32_t* positions, int32_t* slot_of,

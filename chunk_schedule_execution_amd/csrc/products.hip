@@ -1,9 +1,19 @@
 // Products beside the collectives for gfx950: C = act(A B^T + bias) + residual, plain or
 // grouped by expert with ragged sizes, for the forward pass and both gradients.
-#include "product_tile.h"
+#include <algorithm>
+
+#include "products_device.h"
 
 namespace ccl {
 namespace prod {
+
+// Defined with their kernels in product_tile_*.hip and product_rows.hip.
+int launch_tile_bf16(bool a_by_k, bool b_by_k, ProductMode mode, const ProductArgs& g, const ProductPlan& plan,
+                     hipStream_t s, std::string* err);
+int launch_tile_f32(bool a_by_k, bool b_by_k, ProductMode mode, const ProductArgs& g, const ProductPlan& plan,
+                    hipStream_t s, std::string* err);
+int launch_rows(int dtype, const ProductArgs& g, const ProductPlan& plan, hipStream_t s, std::string* err);
+
 namespace {
 
 int hip_status(const char* what, std::string* err) {
@@ -13,223 +23,227 @@ int hip_status(const char* what, std::string* err) {
   return CCL_ERR_HIP;
 }
 
-// ---- one 64 x 64 tile per workgroup -------------------------------------------------
-// Four waves, each 32 x 32 by matrix instructions of 16 x 16. Elements are loaded one by
-// one into LDS rows of 64 bytes along k (80 apart: rows 16 apart then lie on different
-// banks), so any stride and alignment is right. A lane of the matrix instructions holds
-// row (lane & 15) of both operands and the same k values of them: which ones is free as
-// long as A and B agree, so each lane takes 16 consecutive bytes at (lane >> 4) * 16.
-template <typename T, bool AByK, bool BByK>
-__global__ __launch_bounds__(256) void product_any_kernel(ProductArgs g, ProductMode mode, int tiles_n, int tiles_m) {
-  constexpr int BM = 64, BN = 64, BK = 64 / int(sizeof(T)), LD = 80 / int(sizeof(T));
-  constexpr int PER = BM * BK / 256;  // elements per thread and operand
-  __shared__ __attribute__((aligned(16))) T sa[BM * LD];
-  __shared__ __attribute__((aligned(16))) T sb[BN * LD];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const T* A = static_cast<const T*>(g.a);
-  const T* B = static_cast<const T*>(g.b);
-  T* C = static_cast<T*>(g.c);
-  const int64_t tile = blockIdx.x;
-  int group = 0;
-  int64_t row = 0, m_end = g.m, col = 0, k_lo = 0, k_hi = g.k;
-  if (mode == kRaggedK) {
-    const int64_t per = int64_t(tiles_m) * tiles_n;
-    group = int(tile / per);
-    row = (tile % per) / tiles_n * BM;
-    col = (tile % per) % tiles_n * BN;
-    group_bounds(g.offsets, g.k, group, k_lo, k_hi);
-    C += group * g.c_stride;
-  } else {
-    const RowTile t = find_tile(g.offsets, g.groups, g.m, BM, int(tile / tiles_n), true);
-    if (t.group < 0) return;
-    group = t.group;
-    row = t.row;
-    m_end = t.end;
-    col = tile % tiles_n * BN;
-    if (group == g.groups) k_hi = 0;  // rows of no group: zeros
-    else B += group * g.b_stride;
-  }
-  const bool nothing = mode == kRaggedM && group == g.groups;
-  f32x4 acc[2][2] = {};
-  const int wm = (wave >> 1) * 32, wn = (wave & 1) * 32;
-  for (int64_t k0 = k_lo; k0 < k_hi; k0 += BK) {
+// ---- operands off the 16-byte grid ------------------------------------------------------
+// Rows copied to a stride of whole vectors, zeros behind their end. One pass over the
+// operand, so it costs what reading and writing it costs; reading such rows element by
+// element in the tiles costs more from a few tiles per row on.
+template <typename T>
+__global__ __launch_bounds__(256) void regrid_kernel(const T* src, int64_t ld, int64_t rows, int64_t len, T* dst,
+                                                     int64_t ld_dst) {
+  const int64_t c = int64_t(blockIdx.y) * 1024 + threadIdx.x;
+  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x)
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      if (AByK) {
-        const int kk = (i * 256 + tid) / BM, r = (i * 256 + tid) % BM;
-        const bool in = k0 + kk < k_hi && row + r < m_end;
-        sa[r * LD + kk] = in ? A[(k0 + kk) * g.lda + row + r] : T(0.0f);
-      } else {
-        const int kk = (i * 256 + tid) % BK, r = (i * 256 + tid) / BK;
-        const bool in = k0 + kk < k_hi && row + r < m_end;
-        sa[r * LD + kk] = in ? A[(row + r) * g.lda + k0 + kk] : T(0.0f);
-      }
-      if (BByK) {
-        const int kk = (i * 256 + tid) / BN, r = (i * 256 + tid) % BN;
-        const bool in = k0 + kk < k_hi && col + r < g.n;
-        sb[r * LD + kk] = in ? B[(k0 + kk) * g.ldb + col + r] : T(0.0f);
-      } else {
-        const int kk = (i * 256 + tid) % BK, r = (i * 256 + tid) / BK;
-        const bool in = k0 + kk < k_hi && col + r < g.n;
-        sb[r * LD + kk] = in ? B[(col + r) * g.ldb + k0 + kk] : T(0.0f);
-      }
-    }
-    __syncthreads();
-    constexpr int V = 16 / int(sizeof(T));
-    const int at = (lane & 15) * LD + (lane >> 4) * V;
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        // first operand: columns of C, so that a lane ends up with 4 consecutive columns
-        if constexpr (sizeof(T) == 2) {
-          const bf16x8 x = *reinterpret_cast<const bf16x8*>(&sb[(wn + j * 16) * LD + at]);
-          const bf16x8 y = *reinterpret_cast<const bf16x8*>(&sa[(wm + i * 16) * LD + at]);
-          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, y, acc[i][j], 0, 0, 0);
-        } else {
-          const f32x4 x = *reinterpret_cast<const f32x4*>(&sb[(wn + j * 16) * LD + at]);
-          const f32x4 y = *reinterpret_cast<const f32x4*>(&sa[(wm + i * 16) * LD + at]);
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(x[q], y[q], acc[i][j], 0, 0, 0);
-        }
-      }
-    __syncthreads();
-  }
-  const T* bias = g.bias && !nothing ? static_cast<const T*>(g.bias) + group * g.bias_stride : nullptr;
-  const T* residual = static_cast<const T*>(g.residual);
-  T* preact = static_cast<T*>(g.preact);
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int64_t r = row + wm + i * 16 + (lane & 15);
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int64_t c = col + wn + j * 16 + (lane >> 4) * 4 + q;
-        if (r >= m_end || c >= g.n) continue;
-        float z = acc[i][j][q];
-        if (bias) z += widen(bias[c]);
-        if (preact) preact[r * g.ldp + c] = narrow<T>(z);
-        float v = nothing ? 0.0f : act_value(z, g.act);
-        if (residual) v += widen(residual[r * g.ldr + c]);
-        C[r * g.ldc + c] = narrow<T>(v);
-      }
+    for (int i = 0; i < 4; ++i) {
+      const int64_t at = c + i * 256;
+      if (at < ld_dst) dst[r * ld_dst + at] = at < len ? src[r * ld + at] : T(0.0f);
     }
 }
 
+int regrid(int dtype, const void* src, int64_t ld, int64_t rows, int64_t len, void* dst, int64_t ld_dst, hipStream_t s,
+           std::string* err) {
+  const dim3 grid(unsigned(std::min<int64_t>(rows, 1 << 20)), unsigned((ld_dst + 1023) / 1024));
+  if (dtype == CCL_BF16)
+    hipLaunchKernelGGL(regrid_kernel<bf16>, grid, dim3(256), 0, s, static_cast<const bf16*>(src), ld, rows, len,
+                       static_cast<bf16*>(dst), ld_dst);
+  else
+    hipLaunchKernelGGL(regrid_kernel<float>, grid, dim3(256), 0, s, static_cast<const float*>(src), ld, rows, len,
+                       static_cast<float*>(dst), ld_dst);
+  return hip_status("regrid launch", err);
+}
+
+// ---- joining the splits of the summed dimension -------------------------------------------
+constexpr int kJoinRows = 16;
+
 template <typename T>
-int launch_any(bool a_by_k, bool b_by_k, ProductMode mode, const ProductArgs& g, hipStream_t s, std::string* err) {
-  const int64_t tiles_n = (g.n + 63) / 64, tiles_m = (g.m + 63) / 64;
-  // kRaggedM: every group and the rest may end in a tile of their own
-  const int64_t grid = mode == kRaggedK ? g.groups * tiles_m * tiles_n
-                       : mode == kRaggedM ? (tiles_m + g.groups) * tiles_n : tiles_m * tiles_n;
-  if (grid > 0x7fffffff) {
-    *err = "product: more than 2^31 tiles";
-    return CCL_ERR_INVALID_ARGUMENT;
+__global__ __launch_bounds__(256) void join_kernel(ProductArgs g, const float* partial, int splits) {
+  const RowTile t = find_tile(g.offsets, g.groups, g.m, kJoinRows, blockIdx.x, true);
+  const int64_t c = int64_t(blockIdx.y) * 256 + threadIdx.x;
+  if (t.group < 0 || c >= g.n) return;
+  const bool nothing = g.offsets && t.group == g.groups;
+  const int64_t end = min(t.end, t.row + kJoinRows);
+  for (int64_t r = t.row; r < end; ++r) {
+    float z = 0.0f;
+    if (!nothing)
+      for (int s = 0; s < splits; ++s) z += partial[(int64_t(s) * g.m + r) * g.n + c];
+    finish_one<T>(g, z, r, c, t.group, nothing);
   }
-  if (grid == 0) return CCL_OK;
-  auto go = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, dim3(unsigned(grid)), dim3(256), 0, s, g, mode, int(tiles_n), int(tiles_m));
-  };
-  if (a_by_k && b_by_k) go(product_any_kernel<T, true, true>);
-  else if (b_by_k) go(product_any_kernel<T, false, true>);
-  else go(product_any_kernel<T, false, false>);
-  return hip_status("product launch", err);
+}
+
+int join(int dtype, const ProductArgs& g, const float* partial, int splits, hipStream_t s, std::string* err) {
+  const dim3 grid(unsigned((g.m + kJoinRows - 1) / kJoinRows + (g.offsets ? g.groups : 0)), unsigned((g.n + 255) / 256));
+  if (dtype == CCL_BF16) hipLaunchKernelGGL(join_kernel<bf16>, grid, dim3(256), 0, s, g, partial, splits);
+  else hipLaunchKernelGGL(join_kernel<float>, grid, dim3(256), 0, s, g, partial, splits);
+  return hip_status("join launch", err);
 }
 
 // ---- slope and bias gradient ---------------------------------------------------------
-constexpr int kSlopeRows = 64;
+// One pass over dout and preact: a workgroup takes a tile of rows of one group by 256
+// columns, 8 columns (16 or 32 bytes) per thread, and leaves one fp32 sum per column and
+// tile; a second kernel adds the tiles of a group in order, so the sums do not depend on
+// the order in which workgroups run. Bound by memory.
+constexpr int kSlopeLanes = 8;  // rows that a workgroup has in hand at a time
+
+int slope_height(int64_t rows) { return rows < (int64_t(1) << 26) ? 64 : 4096; }
 
 template <typename T>
-__global__ __launch_bounds__(256) void slope_kernel(SlopeArgs g) {
-  const RowTile t = find_tile(g.offsets, g.groups, g.rows, kSlopeRows, blockIdx.x, true);
-  const int64_t c = int64_t(blockIdx.y) * 256 + threadIdx.x;
-  if (t.group < 0 || c >= g.n) return;
+__global__ __launch_bounds__(256) void slope_kernel(SlopeArgs g, int height, bool vec_o, bool vec_p) {
+  __shared__ float sums[kSlopeLanes][256];
+  const RowTile t = find_tile(g.offsets, g.groups, g.rows, height, blockIdx.x, true);
+  if (t.group < 0) return;
+  const int64_t c = int64_t(blockIdx.y) * 256 + (threadIdx.x & 31) * 8;
+  const int n = int(min(int64_t(8), g.n - c)), lane = threadIdx.x >> 5;
   const T* dout = static_cast<const T*>(g.dout);
   const T* preact = static_cast<const T*>(g.preact);
   T* dz = static_cast<T*>(g.dz);
-  float sum = 0.0f;
   const bool nothing = g.offsets && t.group == g.groups;
-  const int64_t end = min(t.end, t.row + kSlopeRows);
-  for (int64_t r = t.row; r < end; ++r) {
-    float v = nothing ? 0.0f : widen(dout[r * g.ldo + c]);
-    if (!nothing && g.act != CCL_ACT_NONE) v *= act_slope(widen(preact[r * g.ldp + c]), g.act);
-    if (dz) dz[r * g.ldz + c] = narrow<T>(v);
-    sum += v;
+  const int64_t end = min(t.end, t.row + height);
+  float sum[8] = {};
+#pragma unroll 2
+  for (int64_t r = t.row + lane; r < end; r += kSlopeLanes) {
+    float v[8] = {};
+    if (!nothing && n > 0) {
+      load8(dout + r * g.ldo + c, vec_o, n, v);
+      if (g.act != CCL_ACT_NONE) {
+        float z[8];
+        load8(preact + r * g.ldp + c, vec_p, n, z);
+        slope8(v, z, g.act);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) v[q] = q < n ? v[q] : 0.0f;
+      }
+    }
+    // the rounding of dz to the operands' type: what a stored gradient has everywhere
+    if (dz && c < g.ldz) store8(dz + r * g.ldz + c, true, int(min(int64_t(8), g.ldz - c)), v);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) sum[q] += v[q];
   }
-  if (g.dbias && !nothing) g.partial[int64_t(t.index) * g.n + c] = sum;
+  if (!g.dbias || nothing) return;
+#pragma unroll
+  for (int q = 0; q < 8; ++q) sums[lane][(threadIdx.x & 31) * 8 + q] = sum[q];
+  __syncthreads();
+  float total = 0.0f;
+#pragma unroll
+  for (int l = 0; l < kSlopeLanes; ++l) total += sums[l][threadIdx.x];
+  const int64_t at = int64_t(blockIdx.y) * 256 + threadIdx.x;
+  if (at < g.n) g.partial[int64_t(t.index) * g.n + at] = total;
 }
 
-// dbias[group][c]: the partial sums of the group's tiles, in the order of the tiles.
+// dbias[group][c]: the partial sums of the group's tiles, 4 interleaved runs of them and
+// then those, always in the same order. A workgroup: 64 columns.
 template <typename T>
-__global__ __launch_bounds__(256) void bias_sum_kernel(SlopeArgs g) {
-  const int group = blockIdx.y;
-  const int64_t c = int64_t(blockIdx.x) * 256 + threadIdx.x;
-  // first tile of the group: tiles of all earlier groups
-  int64_t tile = 0, lo = 0, hi = g.rows;
-  if (g.offsets) {
-    hi = 0;
-    for (int e = 0; e <= group; ++e) {
-      tile += (hi - lo + kSlopeRows - 1) / kSlopeRows;
-      lo = hi;
-      hi = max(lo, int64_t(max(0, min(g.offsets[e + 1], int(g.rows)))));
-    }
-  }
-  if (c >= g.n) return;
-  const int64_t last = tile + (hi - lo + kSlopeRows - 1) / kSlopeRows;
+__global__ __launch_bounds__(256) void bias_sum_kernel(SlopeArgs g, int height) {
+  __shared__ float sums[4][64];
+  const int64_t c = int64_t(blockIdx.x) * 64 + (threadIdx.x & 63);
+  const int run = threadIdx.x >> 6;
+  int64_t first, last;
+  group_tiles(g.offsets, g.groups, g.rows, height, blockIdx.y, first, last);
   float sum = 0.0f;
-  for (; tile < last; ++tile) sum += g.partial[tile * g.n + c];
-  static_cast<T*>(g.dbias)[int64_t(group) * g.n + c] = narrow<T>(sum);
+  if (c < g.n) {
+#pragma unroll 8
+    for (int64_t tile = first + run; tile < last; tile += 4) sum += g.partial[tile * g.n + c];
+  }
+  sums[run][threadIdx.x & 63] = sum;
+  __syncthreads();
+  if (run == 0 && c < g.n)
+    static_cast<T*>(g.dbias)[int64_t(blockIdx.y) * g.n + c] =
+        narrow<T>((sums[0][threadIdx.x] + sums[1][threadIdx.x]) + (sums[2][threadIdx.x] + sums[3][threadIdx.x]));
 }
 
 template <typename T>
 int slope_t(const SlopeArgs& g, hipStream_t s, std::string* err) {
-  const unsigned cols = unsigned((g.n + 255) / 256);
+  const int height = slope_height(g.rows);
+  auto grid16 = [](const void* p, int64_t ld) {
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * sizeof(T) % 16 == 0;
+  };
   if (g.rows > 0 && (g.dz || g.dbias))
-    hipLaunchKernelGGL(slope_kernel<T>, dim3(unsigned(slope_tiles(g.rows, g.offsets ? g.groups : 0)), cols), dim3(256),
-                       0, s, g);
-  if (g.dbias) hipLaunchKernelGGL(bias_sum_kernel<T>, dim3(cols, unsigned(g.groups)), dim3(256), 0, s, g);
+    hipLaunchKernelGGL(slope_kernel<T>,
+                       dim3(unsigned(slope_tiles(g.rows, g.offsets ? g.groups : 0)), unsigned((std::max(g.n, g.ldz) + 255) / 256)),
+                       dim3(256), 0, s, g, height, grid16(g.dout, g.ldo), grid16(g.preact, g.ldp));
+  if (g.dbias)
+    hipLaunchKernelGGL(bias_sum_kernel<T>, dim3(unsigned((g.n + 63) / 64), unsigned(g.groups)), dim3(256), 0, s, g, height);
   return hip_status("bias gradient launch", err);
-}
-
-__global__ __launch_bounds__(256) void fill_zero_kernel(unsigned char* p, int64_t bytes) {
-  for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < bytes; i += int64_t(gridDim.x) * 256) p[i] = 0;
-}
-
-// Whether an operand's stored rows are whole 16-byte vectors.
-bool on_grid(int dtype, bool by_k, const void* p, int64_t ld, int64_t rows, int64_t k) {
-  const int64_t v = dtype == CCL_BF16 ? 8 : 4;
-  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % v == 0 && (by_k ? rows : k) % v == 0;
 }
 
 }  // namespace
 }  // namespace prod
 
-int64_t slope_tiles(int64_t rows, int groups) { return (rows + prod::kSlopeRows - 1) / prod::kSlopeRows + groups; }
+int64_t slope_tiles(int64_t rows, int groups) {
+  const int height = prod::slope_height(rows);
+  return (rows + height - 1) / height + groups;
+}
 
 int launch_slope(int dtype, const SlopeArgs& args, void* stream, std::string* err) {
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   return dtype == CCL_BF16 ? prod::slope_t<prod::bf16>(args, s, err) : prod::slope_t<float>(args, s, err);
 }
 
-int launch_product(int dtype, bool a_by_k, bool b_by_k, ProductMode mode, const ProductArgs& args, void* stream,
-                   std::string* err) {
-  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  if (prod::on_grid(dtype, a_by_k, args.a, args.lda, args.m, args.k) &&
-      prod::on_grid(dtype, b_by_k, args.b, args.ldb, args.n, args.k))
-    return dtype == CCL_BF16 ? prod::launch_tile_bf16(a_by_k, b_by_k, mode, args, s, err)
-                             : prod::launch_tile_f32(a_by_k, b_by_k, mode, args, s, err);
-  return dtype == CCL_BF16 ? prod::launch_any<prod::bf16>(a_by_k, b_by_k, mode, args, s, err)
-                           : prod::launch_any<float>(a_by_k, b_by_k, mode, args, s, err);
+ProductPlan plan_product(int dtype, bool a_by_k, bool b_by_k, ProductMode mode, const ProductArgs& g,
+                         OperandGrid a_grid, OperandGrid b_grid) {
+  ProductPlan p;
+  const int64_t size = dtype == CCL_BF16 ? 2 : 4, v = 16 / size;
+  const bool on_a = a_grid == kPadded || (a_grid == kByStrides && g.lda % v == 0 && (a_by_k ? g.m : g.k) % v == 0);
+  const bool on_b = b_grid == kPadded || (b_grid == kByStrides && g.ldb % v == 0 && (b_by_k ? g.n : g.k) % v == 0);
+  auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
+  // Few rows (on average, in the groups): reading the weights bounds the product, and a
+  // tile of 128 rows would leave most of its products unused.
+  const int64_t mean = g.m / g.groups;
+  if (!a_by_k && !b_by_k && mode != kRaggedK && mean <= 48 && g.m <= 64 * int64_t(g.groups) &&
+      up(g.m, 16) * up(g.n, 16) < (1 << 23)) {
+    p.kind = mean <= 12 && (g.groups > 1 || g.m <= 16) ? kRows16 : mean <= 24 && (g.groups > 1 || g.m <= 32) ? kRows32 : kRows64;
+    p.vec = on_a && on_b;
+    const int64_t height = p.kind == kRows16 ? 16 : p.kind == kRows32 ? 32 : 64;
+    const int64_t bands = up(g.m, height) + (g.groups > 1 ? std::min<int64_t>(g.groups, g.m) : 0);
+    p.columns = bands * up(g.n, 32) >= 512 ? 2 : 1;
+    const int64_t wgs = std::max<int64_t>(1, bands * up(g.n, 16 * p.columns));
+    p.splits = int(std::max<int64_t>(1, std::min<int64_t>(512 / wgs, g.k * size / 4096)));
+  } else {
+    const int64_t groups = mode == kRaggedK ? g.groups : 1;
+    const int64_t rows = mode == kRaggedM ? g.m / g.groups : g.m;  // of one group, on average
+    const int64_t big = up(g.m, 256) * up(g.n, 256) * groups;
+    p.kind = dtype == CCL_BF16 && big >= 200 && rows >= 192 ? kTile256 : kTile128;
+    const int64_t tiles = std::max<int64_t>(
+        1, p.kind == kTile256 ? big : (up(g.m, 128) + (mode == kRaggedM ? g.groups / 2 : 0)) * up(g.n, 128) * groups);
+    const int64_t steps = up(g.k, 128 / size);
+    if (mode != kRaggedK && tiles < 192) p.splits = int(std::max<int64_t>(1, std::min({up(384, tiles), steps / 4, int64_t(16)})));
+    p.copy_a = !on_a;
+    p.copy_b = !on_b;
+    p.ld_a = up(a_by_k ? g.m : g.k, v) * v;
+    p.ld_b = up(b_by_k ? g.n : g.k, v) * v;
+  }
+  // bytes of the copies: every stored row
+  const int64_t rows_a = a_by_k ? g.k : g.m;
+  const int64_t rows_b = (b_by_k ? g.k : g.n) * (mode == kRaggedM ? g.groups : 1);
+  p.at_b = p.copy_a ? up(rows_a * p.ld_a * size, 16) * 16 : 0;
+  p.at_partial = p.at_b + (p.copy_b ? up(rows_b * p.ld_b * size, 16) * 16 : 0);
+  p.bytes = p.at_partial + (p.splits > 1 ? p.splits * g.m * g.n * 4 : 0);
+  return p;
 }
 
-int launch_fill_zero(void* p, int64_t bytes, void* stream, std::string* err) {
-  if (bytes <= 0) return CCL_OK;
-  const unsigned grid = unsigned(std::min<int64_t>(1024, (bytes + 255) / 256));
-  hipLaunchKernelGGL(prod::fill_zero_kernel, dim3(grid), dim3(256), 0, reinterpret_cast<hipStream_t>(stream),
-                     static_cast<unsigned char*>(p), bytes);
-  return prod::hip_status("fill launch", err);
+int launch_product(int dtype, bool a_by_k, bool b_by_k, ProductMode mode, const ProductArgs& args,
+                   const ProductPlan& plan, void* workspace, void* stream, std::string* err) {
+  using namespace prod;
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  ProductArgs g = args;
+  unsigned char* ws = static_cast<unsigned char*>(workspace);
+  if (plan.copy_a) {
+    if (int rc = regrid(dtype, g.a, g.lda, a_by_k ? g.k : g.m, a_by_k ? g.m : g.k, ws + plan.at_a, plan.ld_a, s, err)) return rc;
+    g.a = ws + plan.at_a;
+    g.lda = plan.ld_a;
+  }
+  if (plan.copy_b) {
+    // the groups' matrices follow each other, so their rows are one run of rows
+    const int64_t rows = (b_by_k ? g.k : g.n) * (mode == kRaggedM ? g.groups : 1);
+    if (int rc = regrid(dtype, g.b, g.ldb, rows, b_by_k ? g.n : g.k, ws + plan.at_b, plan.ld_b, s, err)) return rc;
+    g.b = ws + plan.at_b;
+    g.ldb = plan.ld_b;
+    g.b_stride = (b_by_k ? g.k : g.n) * plan.ld_b;
+  }
+  if (plan.splits > 1) g.partial = reinterpret_cast<float*>(ws + plan.at_partial);
+  int rc;
+  if (plan.kind == kRows16 || plan.kind == kRows32 || plan.kind == kRows64) rc = launch_rows(dtype, g, plan, s, err);
+  else if (dtype == CCL_BF16) rc = launch_tile_bf16(a_by_k, b_by_k, mode, g, plan, s, err);
+  else rc = launch_tile_f32(a_by_k, b_by_k, mode, g, plan, s, err);
+  if (rc || plan.splits == 1) return rc;
+  return join(dtype, g, g.partial, plan.splits, s, err);
 }
 
 }  // namespace ccl

@@ -151,5 +151,124 @@ __device__ inline void group_bounds(const int32_t* offsets, int64_t rows, int gr
   hi = max(top, min(offsets[group + 1], int(rows)));
 }
 
+// The numbers of a group's tiles of `height` rows, [first, last).
+__device__ inline void group_tiles(const int32_t* offsets, int groups, int64_t rows, int height, int group,
+                                   int64_t& first, int64_t& last) {
+  first = 0;
+  if (offsets == nullptr) {
+    last = (rows + height - 1) / height;
+    return;
+  }
+  const int lane = threadIdx.x & 63;
+  int carry_tiles = 0, carry_max = 0;
+  for (int base = 0; base <= group; base += 64) {
+    const int e = base + lane;
+    int hi = e < groups ? max(0, min(offsets[e + 1], int(rows))) : 0;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int v = __shfl_up(hi, d);
+      if (lane >= d) hi = max(hi, v);
+    }
+    hi = max(hi, carry_max);
+    int lo = __shfl_up(hi, 1);
+    if (lane == 0) lo = carry_max;
+    const int tiles = int((int64_t(hi) - lo + height - 1) / height);
+    int upto = tiles;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int v = __shfl_up(upto, d);
+      if (lane >= d) upto += v;
+    }
+    upto += carry_tiles;
+    if (group < base + 64) {
+      last = __builtin_amdgcn_readlane(upto, group - base);
+      first = last - __builtin_amdgcn_readlane(tiles, group - base);
+    }
+    carry_tiles = __builtin_amdgcn_readlane(upto, 63);
+    carry_max = __builtin_amdgcn_readlane(hi, 63);
+  }
+}
+
+// ---- results -----------------------------------------------------------------------------
+// 8 neighbouring values of a row; `vec`: the row lies on the 16-byte grid; `n`: how many of
+// them exist.
+template <typename T>
+__device__ inline void load8(const T* p, bool vec, int n, float* v) {
+  if (vec && n >= 8) {
+    constexpr int V = 16 / int(sizeof(T));
+    typedef T pack __attribute__((ext_vector_type(V)));
+#pragma unroll
+    for (int h = 0; h < 8 / V; ++h) {
+      const pack x = reinterpret_cast<const pack*>(p)[h];
+#pragma unroll
+      for (int q = 0; q < V; ++q) v[h * V + q] = widen(x[q]);
+    }
+  } else {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) v[q] = q < n ? widen(p[q]) : 0.0f;
+  }
+}
+template <typename T>
+__device__ inline void store8(T* p, bool vec, int n, const float* v) {
+  if (vec && n >= 8) {
+    constexpr int V = 16 / int(sizeof(T));
+    typedef T pack __attribute__((ext_vector_type(V)));
+#pragma unroll
+    for (int h = 0; h < 8 / V; ++h) {
+      pack x;
+#pragma unroll
+      for (int q = 0; q < V; ++q) x[q] = narrow<T>(v[h * V + q]);
+      reinterpret_cast<pack*>(p)[h] = x;
+    }
+  } else {
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      if (q < n) p[q] = narrow<T>(v[q]);
+  }
+}
+// The activation of 8 values: the branch is taken once for them.
+__device__ inline void act8(float* v, int act) {
+#define CCL_ACT8(A)                                            \
+  case A:                                                      \
+    _Pragma("unroll") for (int q = 0; q < 8; ++q) v[q] = act_value(v[q], A); \
+    break;
+  switch (act) {
+    CCL_ACT8(CCL_ACT_RELU)
+    CCL_ACT8(CCL_ACT_GELU)
+    CCL_ACT8(CCL_ACT_GELU_TANH)
+    CCL_ACT8(CCL_ACT_SILU)
+    default: break;
+  }
+#undef CCL_ACT8
+}
+// v times the slopes at z.
+__device__ inline void slope8(float* v, const float* z, int act) {
+#define CCL_SLOPE8(A)                                                            \
+  case A:                                                                        \
+    _Pragma("unroll") for (int q = 0; q < 8; ++q) v[q] *= act_slope(z[q], A);    \
+    break;
+  switch (act) {
+    CCL_SLOPE8(CCL_ACT_RELU)
+    CCL_SLOPE8(CCL_ACT_GELU)
+    CCL_SLOPE8(CCL_ACT_GELU_TANH)
+    CCL_SLOPE8(CCL_ACT_SILU)
+    default: break;
+  }
+#undef CCL_SLOPE8
+}
+
+// bias, activation, residual and stores of one result z of column c.
+template <typename T>
+__device__ inline void finish_one(const ProductArgs& g, float z, int64_t row, int64_t c, int group, bool nothing) {
+  float v = 0.0f;
+  if (!nothing) {
+    if (g.bias) z += widen(static_cast<const T*>(g.bias)[group * g.bias_stride + c]);
+    v = act_value(z, g.act);
+  }
+  if (g.preact) static_cast<T*>(g.preact)[row * g.ldp + c] = narrow<T>(nothing ? 0.0f : z);
+  if (g.residual) v += widen(static_cast<const T*>(g.residual)[row * g.ldr + c]);
+  static_cast<T*>(g.c)[row * g.ldc + c] = narrow<T>(v);
+}
+
 }  // namespace prod
 }  // namespace ccl

@@ -23,51 +23,73 @@ ACTIVATIONS = {"none": capi.CCL_ACT_NONE, "relu": capi.CCL_ACT_RELU, "gelu": cap
 
 
 # ---- arguments ----------------------------------------------------------------------
-def _check(ok: bool, what: str) -> None:
-    if not ok:
-        raise ValueError(what)
+# These run on every call, in front of kernels that take a few microseconds: one look at
+# each property, and messages are made only for what is refused.
+def _refuse(what: str):
+    raise ValueError(what)
 
 
-def _float(t: torch.Tensor, name: str, shape, like: torch.Tensor | None = None) -> torch.Tensor:
-    _check(isinstance(t, torch.Tensor), f"{name}: a tensor wanted")
-    _check(t.dtype in DTYPES, f"{name}: float32 or bfloat16 wanted, not {t.dtype}")
-    _check(tuple(t.shape) == tuple(shape), f"{name}: shape {tuple(shape)} wanted, not {tuple(t.shape)}")
-    if like is not None:
-        _check(t.dtype == like.dtype, f"{name}: {like.dtype} wanted, not {t.dtype}")
-        _check(t.device == like.device, f"{name}: on {t.device}, not {like.device}")
-    _check(t.device.type == "cuda", f"{name}: on {t.device}; GPU memory wanted")
-    return t
+def _first(t, name: str) -> int:
+    """The device index of the matrix that the other arguments have to match."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        _refuse(f"{name}: a matrix wanted")
+    if t.dtype not in DTYPES:
+        _refuse(f"{name}: float32 or bfloat16 wanted, not {t.dtype}")
+    if not t.is_cuda:
+        _refuse(f"{name}: on {t.device}; GPU memory wanted")
+    return t.get_device()
 
 
-def _index(t: torch.Tensor, name: str, shape, like: torch.Tensor) -> torch.Tensor:
-    _check(isinstance(t, torch.Tensor) and t.dtype == torch.int32, f"{name}: an int32 tensor wanted")
-    _check(tuple(t.shape) == tuple(shape), f"{name}: shape {tuple(shape)} wanted, not {tuple(t.shape)}")
-    _check(t.device == like.device and t.device.type == "cuda", f"{name}: on {t.device}, not {like.device}")
-    _check(t.is_contiguous(), f"{name}: contiguous wanted")
-    return t
+def _like(t, name: str, shape, dtype, device: int) -> None:
+    if not isinstance(t, torch.Tensor):
+        _refuse(f"{name}: a tensor wanted")
+    if t.dtype is not dtype:
+        _refuse(f"{name}: {dtype} wanted, not {t.dtype}")
+    if t.shape != shape:
+        _refuse(f"{name}: shape {tuple(shape)} wanted, not {tuple(t.shape)}")
+    if not t.is_cuda or t.get_device() != device:
+        _refuse(f"{name}: on {t.device}; memory of GPU {device} wanted")
 
 
-def _ld(t: torch.Tensor | None, name: str) -> int:
-    """Distance between the rows of a matrix (0: packed, or a single row)."""
-    if t is None or t.numel() == 0:
-        return 0
-    _check(t.shape[-1] == 1 or t.stride(-1) == 1, f"{name}: rows must be contiguous")
-    if t.dim() == 3 and t.shape[1] == 1:
-        ld = t.stride(0) if t.shape[0] > 1 else 0
+def _packed(t, name: str, shape, dtype, device: int) -> int:
+    """Address of a contiguous tensor."""
+    _like(t, name, shape, dtype, device)
+    if not t.is_contiguous():
+        _refuse(f"{name}: contiguous wanted")
+    return t.data_ptr()
+
+
+def _ld(t, name: str) -> int:
+    """Distance between the rows of a matrix, or of matrices that follow each other (0:
+    there is one row, or none)."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) == 2:
+        rows, width = shape
+        if rows <= 1 or width == 0:
+            if width > 1 and rows and stride[1] != 1:
+                _refuse(f"{name}: rows must be contiguous")
+            return 0
+        ld = stride[0]
     else:
-        ld = t.stride(-2) if t.shape[-2] > 1 else 0
-        if t.dim() == 3 and t.shape[0] > 1:
-            _check(t.stride(0) == t.shape[1] * ld, f"{name}: the experts' matrices must follow each other")
-    several = t.shape[-2] > 1 or (t.dim() == 3 and t.shape[0] > 1)
-    _check(not several or ld >= t.shape[-1], f"{name}: rows must not overlap")
+        experts, rows, width = shape
+        if experts * rows <= 1 or width == 0:
+            ld = 0
+        elif rows == 1:
+            ld = stride[0]
+        else:
+            ld = stride[1]
+            if experts > 1 and stride[0] != rows * ld:
+                _refuse(f"{name}: the experts' matrices must follow each other")
+        if ld == 0 and experts * rows > 1:
+            _refuse(f"{name}: rows must not overlap")
+    if width > 1 and stride[-1] != 1:
+        _refuse(f"{name}: rows must be contiguous")
+    if 0 <= ld < width and (ld or len(shape) == 2):
+        _refuse(f"{name}: rows must not overlap")
     return ld
 
 
-def _ptr(t: torch.Tensor | None) -> int:
-    return 0 if t is None else t.data_ptr()
-
-
-def _stream(stream, device) -> int:
+def _stream(stream, device: int) -> int:
     if stream is None:
         return torch.cuda.current_stream(device).cuda_stream
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
@@ -76,8 +98,6 @@ def _stream(stream, device) -> int:
 def _own(stream, *tensors) -> None:
     """Tells torch's allocator that memory allocated on its current stream is in use on
     ``stream``, so it is not handed out again before that stream passes the call."""
-    if stream is None:
-        return
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
     for t in tensors:
@@ -85,20 +105,26 @@ def _own(stream, *tensors) -> None:
             t.record_stream(stream)
 
 
-def _workspace(nbytes: int, device) -> torch.Tensor | None:
+class _on:
+    """The device of a call, made current if it is not."""
+
+    __slots__ = ("device", "before")
+
+    def __init__(self, device: int):
+        self.device = device
+
+    def __enter__(self):
+        self.before = torch.cuda.current_device()
+        if self.before != self.device:
+            torch.cuda.set_device(self.device)
+
+    def __exit__(self, *a):
+        if self.before != self.device:
+            torch.cuda.set_device(self.before)
+
+
+def _workspace(nbytes: int, device):
     return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
-
-
-def _desc(x_shape, out_features, dtype, activation, experts, tensors, **ld) -> capi.ccl_linear_desc:
-    _check(activation in ACTIVATIONS, f"unknown activation {activation!r}")
-    flags = 0
-    if any(t is not None and t.data_ptr() % 16 for t in tensors):
-        flags |= capi.CCL_LINEAR_UNALIGNED
-    d = capi.ccl_linear_desc(dtype=DTYPES[dtype], activation=ACTIVATIONS[activation], rows=x_shape[0],
-                             in_features=x_shape[1], out_features=out_features, experts=experts, flags=flags)
-    for name, value in ld.items():
-        setattr(d, name, value)
-    return d
 
 
 # ---- products -----------------------------------------------------------------------
@@ -118,47 +144,56 @@ def grouped_linear(x, w, offsets, bias=None, activation="none", save_preact=Fals
     return _forward(x, w, offsets, bias, None, activation, save_preact, out, preact, stream)
 
 
+def _weights(w, x, grouped: bool):
+    """(experts, out_features) of w, which has to match x (rows, in)."""
+    if not isinstance(w, torch.Tensor) or w.dim() != (3 if grouped else 2):
+        _refuse("w: (experts, out, in) wanted" if grouped else "w: (out, in) wanted")
+    return (w.shape[0] if grouped else 0), w.shape[-2]
+
+
 def _forward(x, w, offsets, bias, residual, activation, save_preact, out, preact, stream):
-    grouped = offsets is not None
-    _check(isinstance(x, torch.Tensor) and x.dim() == 2, "x: a matrix wanted")
-    _check(isinstance(w, torch.Tensor) and w.dim() == (3 if grouped else 2),
-           "w: (experts, out, in) wanted" if grouped else "w: (out, in) wanted")
+    device, grouped = _first(x, "x"), offsets is not None
+    experts, n = _weights(w, x, grouped)
     rows, k = x.shape
-    n = w.shape[-2]
-    experts = w.shape[0] if grouped else 1
-    _float(x, "x", x.shape)
-    _float(w, "w", (experts, n, k) if grouped else (n, k), x)
-    if grouped:
-        _index(offsets, "offsets", (experts + 1,), x)
-    if bias is not None:
-        _float(bias, "bias", (experts, n) if grouped else (n,), x)
-        _check(bias.is_contiguous(), "bias: contiguous wanted")
+    dtype = x.dtype
+    _like(w, "w", (experts, n, k) if grouped else (n, k), dtype, device)
+    if activation not in ACTIVATIONS:
+        _refuse(f"unknown activation {activation!r}")
+    px, pw = x.data_ptr(), w.data_ptr()
+    po = _packed(offsets, "offsets", (experts + 1,), torch.int32, device) if grouped else 0
+    pb = 0 if bias is None else _packed(bias, "bias", (experts, n) if grouped else (n,), dtype, device)
+    pr = ldr = pp = ldp = ldo = 0
     if residual is not None:
-        _float(residual, "residual", (rows, n), x)
-    made = []
-    if out is None:
-        out = torch.empty(rows, n, dtype=x.dtype, device=x.device)
-        made.append(out)
-    _float(out, "out", (rows, n), x)
-    if preact is None and save_preact:
-        preact = torch.empty(rows, n, dtype=x.dtype, device=x.device)
-        made.append(preact)
-    if preact is not None:
-        _float(preact, "preact", (rows, n), x)
-    d = _desc(x.shape, n, x.dtype, activation, experts if grouped else 0, (x, w, bias, residual, out, preact),
-              ld_x=_ld(x, "x"), ld_w=_ld(w, "w"), ld_out=_ld(out, "out"), ld_residual=_ld(residual, "residual"),
-              ld_preact=_ld(preact, "preact"))
-    nbytes = capi.ccl_linear_workspace(d, grouped, False)
-    with torch.cuda.device(x.device):
-        ws = _workspace(nbytes, x.device)
-        s = _stream(stream, x.device)
-        if grouped:
-            capi.ccl_grouped_linear(d, _ptr(offsets), _ptr(x), _ptr(w), _ptr(bias), _ptr(out), _ptr(preact), _ptr(ws),
-                                    nbytes, s)
+        _like(residual, "residual", (rows, n), dtype, device)
+        pr, ldr = residual.data_ptr(), _ld(residual, "residual")
+    with _on(device):
+        made_out = out is None
+        if made_out:
+            out = torch.empty(rows, n, dtype=dtype, device=x.device)
         else:
-            capi.ccl_linear(d, _ptr(x), _ptr(w), _ptr(bias), _ptr(residual), _ptr(out), _ptr(preact), _ptr(ws),
-                            nbytes, s)
-        _own(stream, ws, *made)
+            _like(out, "out", (rows, n), dtype, device)
+            ldo = _ld(out, "out")
+        pout = out.data_ptr()
+        made_preact = preact is None and save_preact
+        if made_preact:
+            preact = torch.empty(rows, n, dtype=dtype, device=x.device)
+        elif preact is not None:
+            _like(preact, "preact", (rows, n), dtype, device)
+            ldp = _ld(preact, "preact")
+        if preact is not None:
+            pp = preact.data_ptr()
+        d = capi.ccl_linear_desc(DTYPES[dtype], ACTIVATIONS[activation], rows, k, n, experts,
+                                 capi.CCL_LINEAR_UNALIGNED if (px | pw | pb | pr | pout | pp) % 16 else 0,
+                                 _ld(x, "x"), _ld(w, "w"), ldo, ldr, ldp)
+        nbytes = capi.ccl_linear_workspace(d, grouped, False)
+        ws = _workspace(nbytes, x.device)
+        pws, s = (ws.data_ptr() if nbytes else 0), _stream(stream, device)
+        if grouped:
+            capi.ccl_grouped_linear(d, po, px, pw, pb, pout, pp, pws, nbytes, s)
+        else:
+            capi.ccl_linear(d, px, pw, pb, pr, pout, pp, pws, nbytes, s)
+        if stream is not None:
+            _own(stream, ws, out if made_out else None, preact if made_preact else None)
     return out if preact is None else (out, preact)
 
 
@@ -177,38 +212,39 @@ def grouped_linear_backward(dout, x, w, offsets, preact=None, activation="none",
 
 
 def _backward(dout, x, w, offsets, preact, activation, bias, need_dx, need_dw, stream):
-    grouped = offsets is not None
-    _check(isinstance(x, torch.Tensor) and x.dim() == 2, "x: a matrix wanted")
-    _check(isinstance(w, torch.Tensor) and w.dim() == (3 if grouped else 2),
-           "w: (experts, out, in) wanted" if grouped else "w: (out, in) wanted")
+    device, grouped = _first(x, "x"), offsets is not None
+    experts, n = _weights(w, x, grouped)
     rows, k = x.shape
-    n = w.shape[-2]
-    experts = w.shape[0] if grouped else 1
-    _float(x, "x", x.shape)
-    _float(w, "w", (experts, n, k) if grouped else (n, k), x)
-    _float(dout, "dout", (rows, n), x)
-    if grouped:
-        _index(offsets, "offsets", (experts + 1,), x)
-    _check(activation == "none" or preact is not None, "the activation's gradient needs preact")
-    if activation == "none":
-        preact = None
-    if preact is not None:
-        _float(preact, "preact", (rows, n), x)
-    dx = torch.empty(rows, k, dtype=x.dtype, device=x.device) if need_dx else None
-    dw = torch.empty(w.shape, dtype=x.dtype, device=x.device) if need_dw else None
-    db = torch.empty(w.shape[:-1], dtype=x.dtype, device=x.device) if bias else None
-    d = _desc(x.shape, n, x.dtype, activation, experts if grouped else 0, (dout, x, w, preact, dx, dw, db),
-              ld_x=_ld(x, "x"), ld_w=_ld(w, "w"), ld_out=_ld(dout, "dout"), ld_preact=_ld(preact, "preact"))
-    nbytes = capi.ccl_linear_workspace(d, grouped, True)
-    with torch.cuda.device(x.device):
+    dtype = x.dtype
+    _like(w, "w", (experts, n, k) if grouped else (n, k), dtype, device)
+    _like(dout, "dout", (rows, n), dtype, device)
+    if activation not in ACTIVATIONS:
+        _refuse(f"unknown activation {activation!r}")
+    px, pw, pd = x.data_ptr(), w.data_ptr(), dout.data_ptr()
+    po = _packed(offsets, "offsets", (experts + 1,), torch.int32, device) if grouped else 0
+    pp = ldp = 0
+    if activation != "none":
+        if preact is None:
+            _refuse("the activation's gradient needs preact")
+        _like(preact, "preact", (rows, n), dtype, device)
+        pp, ldp = preact.data_ptr(), _ld(preact, "preact")
+    with _on(device):
+        dx = torch.empty(rows, k, dtype=dtype, device=x.device) if need_dx else None
+        dw = torch.empty(w.shape, dtype=dtype, device=x.device) if need_dw else None
+        db = torch.empty(w.shape[:-1], dtype=dtype, device=x.device) if bias else None
+        d = capi.ccl_linear_desc(DTYPES[dtype], ACTIVATIONS[activation], rows, k, n, experts,
+                                 capi.CCL_LINEAR_UNALIGNED if (px | pw | pd | pp) % 16 else 0,
+                                 _ld(x, "x"), _ld(w, "w"), _ld(dout, "dout"), 0, ldp)
+        nbytes = capi.ccl_linear_workspace(d, grouped, True)
         ws = _workspace(nbytes, x.device)
-        s = _stream(stream, x.device)
-        tail = (_ptr(dout), _ptr(x), _ptr(w), _ptr(preact), _ptr(dx), _ptr(dw), _ptr(db), _ptr(ws), nbytes, s)
+        tail = (pd, px, pw, pp, dx.data_ptr() if need_dx else 0, dw.data_ptr() if need_dw else 0,
+                db.data_ptr() if bias else 0, ws.data_ptr() if nbytes else 0, nbytes, _stream(stream, device))
         if grouped:
-            capi.ccl_grouped_linear_backward(d, _ptr(offsets), *tail)
+            capi.ccl_grouped_linear_backward(d, po, *tail)
         else:
             capi.ccl_linear_backward(d, *tail)
-        _own(stream, ws, dx, dw, db)
+        if stream is not None:
+            _own(stream, ws, dx, dw, db)
     return [t for t in (dx, dw, db) if t is not None]
 
 
@@ -218,36 +254,45 @@ def expert_route(ids, experts, stream=None):
     slots (tokens * choices)), int32: rows ordered by expert and, within an expert, by slot
     (the index of a choice in ids). positions: a choice's row, -1 where its id is not in
     [0, experts); slots: a row's choice, -1 for the rows from offsets[experts] on."""
-    _check(isinstance(ids, torch.Tensor) and ids.dim() == 2, "ids: (tokens, choices) wanted")
-    _index(ids, "ids", ids.shape, ids)
+    if not isinstance(ids, torch.Tensor) or ids.dim() != 2:
+        _refuse("ids: (tokens, choices) wanted")
+    device = ids.get_device()
+    pi = _packed(ids, "ids", ids.shape, torch.int32, device)
     tokens, choices = ids.shape
     nbytes = capi.ccl_expert_route_workspace(tokens, choices, experts)
-    with torch.cuda.device(ids.device):
+    with _on(device):
         offsets = torch.empty(experts + 1, dtype=torch.int32, device=ids.device)
         positions = torch.empty_like(ids)
         slots = torch.empty(tokens * choices, dtype=torch.int32, device=ids.device)
         ws = _workspace(nbytes, ids.device)
-        capi.ccl_expert_route(_ptr(ids), tokens, choices, experts, _ptr(offsets), _ptr(positions), _ptr(slots),
-                              _ptr(ws), nbytes, _stream(stream, ids.device))
-        _own(stream, ws, offsets, positions, slots)
+        capi.ccl_expert_route(pi, tokens, choices, experts, offsets.data_ptr(), positions.data_ptr(),
+                              slots.data_ptr(), ws.data_ptr() if nbytes else 0, nbytes, _stream(stream, device))
+        if stream is not None:
+            _own(stream, ws, offsets, positions, slots)
     return offsets, positions, slots
+
+
+def _gates(gates, positions, device: int) -> int:
+    return 0 if gates is None else _packed(gates, "gates", positions.shape, torch.float32, device)
 
 
 def expert_dispatch(x, slots, choices, out=None, stream=None):
     """rows[i] = x[slots[i] // choices], zeros where slots[i] is -1: x (tokens, width), rows
     (tokens * choices, width)."""
-    _check(isinstance(x, torch.Tensor) and x.dim() == 2, "x: a matrix wanted")
+    device = _first(x, "x")
     tokens, width = x.shape
-    _float(x, "x", x.shape)
-    _index(slots, "slots", (tokens * choices,), x)
-    with torch.cuda.device(x.device):
-        made = out is None
+    ps = _packed(slots, "slots", (tokens * choices,), torch.int32, device)
+    with _on(device):
+        made, ldo = out is None, 0
         if made:
             out = torch.empty(tokens * choices, width, dtype=x.dtype, device=x.device)
-        _float(out, "out", (tokens * choices, width), x)
-        capi.ccl_expert_dispatch(DTYPES[x.dtype], _ptr(x), _ld(x, "x"), _ptr(slots), tokens, choices, width, _ptr(out),
-                                 _ld(out, "out"), _stream(stream, x.device))
-        _own(stream, out if made else None)
+        else:
+            _like(out, "out", (tokens * choices, width), x.dtype, device)
+            ldo = _ld(out, "out")
+        capi.ccl_expert_dispatch(DTYPES[x.dtype], x.data_ptr(), _ld(x, "x"), ps, tokens, choices, width,
+                                 out.data_ptr(), ldo, _stream(stream, device))
+        if stream is not None and made:
+            _own(stream, out)
     return out
 
 
@@ -255,47 +300,47 @@ def expert_combine(h, positions, gates=None, out=None, stream=None):
     """out[t] = sum over j of gates[t, j] h[positions[t, j]]: h (tokens * choices, width),
     gates (tokens, choices) float32 or None for ones. Without gates it is also the gradient
     of ``expert_dispatch``'s x from its rows' gradients."""
-    _check(isinstance(h, torch.Tensor) and h.dim() == 2, "h: a matrix wanted")
-    _check(isinstance(positions, torch.Tensor) and positions.dim() == 2, "positions: (tokens, choices) wanted")
+    device = _first(h, "h")
+    if not isinstance(positions, torch.Tensor) or positions.dim() != 2:
+        _refuse("positions: (tokens, choices) wanted")
     tokens, choices = positions.shape
     width = h.shape[1]
-    _float(h, "h", (tokens * choices, width))
-    _index(positions, "positions", positions.shape, h)
-    if gates is not None:
-        _float(gates, "gates", positions.shape)
-        _check(gates.dtype == torch.float32 and gates.is_contiguous() and gates.device == h.device,
-               "gates: contiguous float32 on h's device wanted")
-    with torch.cuda.device(h.device):
-        made = out is None
+    _like(h, "h", (tokens * choices, width), h.dtype, device)
+    pp = _packed(positions, "positions", positions.shape, torch.int32, device)
+    pg = _gates(gates, positions, device)
+    with _on(device):
+        made, ldo = out is None, 0
         if made:
             out = torch.empty(tokens, width, dtype=h.dtype, device=h.device)
-        _float(out, "out", (tokens, width), h)
-        capi.ccl_expert_combine(DTYPES[h.dtype], _ptr(h), _ld(h, "h"), _ptr(positions), _ptr(gates), tokens, choices,
-                                width, _ptr(out), _ld(out, "out"), _stream(stream, h.device))
-        _own(stream, out if made else None)
+        else:
+            _like(out, "out", (tokens, width), h.dtype, device)
+            ldo = _ld(out, "out")
+        capi.ccl_expert_combine(DTYPES[h.dtype], h.data_ptr(), _ld(h, "h"), pp, pg, tokens, choices, width,
+                                out.data_ptr(), ldo, _stream(stream, device))
+        if stream is not None and made:
+            _own(stream, out)
     return out
 
 
 def expert_combine_backward(dout, h, positions, slots, gates=None, stream=None):
     """Gradients of ``expert_combine``: dh (tokens * choices, width) and dgates (tokens,
     choices) float32; positions and slots are the route's."""
-    _check(isinstance(dout, torch.Tensor) and dout.dim() == 2, "dout: a matrix wanted")
-    _check(isinstance(positions, torch.Tensor) and positions.dim() == 2, "positions: (tokens, choices) wanted")
+    device = _first(dout, "dout")
+    if not isinstance(positions, torch.Tensor) or positions.dim() != 2:
+        _refuse("positions: (tokens, choices) wanted")
     tokens, choices = positions.shape
     width = dout.shape[1]
-    _float(dout, "dout", (tokens, width))
-    _float(h, "h", (tokens * choices, width), dout)
-    _index(positions, "positions", positions.shape, dout)
-    _index(slots, "slots", (tokens * choices,), dout)
-    if gates is not None:
-        _float(gates, "gates", positions.shape)
-        _check(gates.dtype == torch.float32 and gates.is_contiguous() and gates.device == h.device,
-               "gates: contiguous float32 on h's device wanted")
-    with torch.cuda.device(h.device):
+    _like(dout, "dout", (tokens, width), dout.dtype, device)
+    _like(h, "h", (tokens * choices, width), dout.dtype, device)
+    pp = _packed(positions, "positions", positions.shape, torch.int32, device)
+    ps = _packed(slots, "slots", (tokens * choices,), torch.int32, device)
+    pg = _gates(gates, positions, device)
+    with _on(device):
         dh = torch.empty(tokens * choices, width, dtype=h.dtype, device=h.device)
         dgates = torch.empty(tokens, choices, dtype=torch.float32, device=h.device)
-        capi.ccl_expert_combine_backward(DTYPES[h.dtype], _ptr(dout), _ld(dout, "dout"), _ptr(h), _ld(h, "h"),
-                                         _ptr(positions), _ptr(slots), _ptr(gates), tokens, choices, width, _ptr(dh),
-                                         0, _ptr(dgates), _stream(stream, h.device))
-        _own(stream, dh, dgates)
+        capi.ccl_expert_combine_backward(DTYPES[h.dtype], dout.data_ptr(), _ld(dout, "dout"), h.data_ptr(),
+                                         _ld(h, "h"), pp, ps, pg, tokens, choices, width, dh.data_ptr(), 0,
+                                         dgates.data_ptr(), _stream(stream, device))
+        if stream is not None:
+            _own(stream, dh, dgates)
     return dh, dgates

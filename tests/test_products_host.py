@@ -119,6 +119,16 @@ def test_workspace_is_checked():
         refused(capi.CCL_ERR_INVALID_ARGUMENT, capi.ccl_linear_backward, d, *args.values(), ws, have)
 
 
+@pytest.mark.parametrize("dtype", [capi.CCL_F32, capi.CCL_BF16])
+@pytest.mark.parametrize("experts", [0, 1, 64, 4096])
+@pytest.mark.parametrize("rows", [0, 1, 17, 1000, 2**31 - 1])
+def test_workspace_of_every_size(rows, experts, dtype):
+    for k, n in ((1, 1), (8, 8), (33, 1 << 20), (1 << 20, 33), (4096, 4096)):
+        for backward in (False, True):
+            d = desc(dtype=dtype, rows=rows, in_features=k, out_features=n, experts=experts)
+            assert capi.ccl_linear_workspace(d, experts > 0, backward) >= 0
+
+
 def test_workspace_grows_with_the_rows():
     last = -1
     for rows in (0, 1, 100, 10000, 1 << 20):
