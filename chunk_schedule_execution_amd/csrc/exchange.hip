@@ -1,6 +1,8 @@
 // The row exchange around an expert-parallel layer's AllToAlls for gfx950: routing (a
 // stable counting sort of the choices by expert), dispatch, combine and its gradients.
 // All of it is memory traffic; rows move as 16-byte vectors where they lie on that grid.
+#include <algorithm>
+
 #include "products_device.h"
 
 namespace ccl {
@@ -104,6 +106,48 @@ __global__ __launch_bounds__(64) void route_place_kernel(const int32_t* ids, int
   for (int64_t i = max(lo, used) + threadIdx.x; i < hi; i += 64) slot_of[i] = -1;
 }
 
+// A whole route in one workgroup, for few slots: the chunks are its 16 waves'.
+__global__ __launch_bounds__(1024) void route_small_kernel(const int32_t* ids, int slots, int experts, int bits,
+                                                           int32_t* offsets, int32_t* positions, int32_t* slot_of) {
+  __shared__ int count[16][kMaxExperts];
+  __shared__ int wave_total[16];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  for (int e = lane; e < experts; e += 64) count[wave][e] = 0;
+  const int chunk = ((slots + 15) / 16 + 63) / 64 * 64;
+  const int lo = min(slots, wave * chunk), hi = min(slots, lo + chunk);
+  __builtin_amdgcn_wave_barrier();
+  walk_chunk<false>(ids, lo, hi, experts, bits, count[wave], nullptr, nullptr);
+  __syncthreads();
+  int sum = 0;
+  if (tid < experts)
+    for (int w = 0; w < 16; ++w) sum += count[w][tid];
+  int upto = sum;  // of this and the earlier experts
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int v = __shfl_up(upto, d);
+    if (lane >= d) upto += v;
+  }
+  if (lane == 63) wave_total[wave] = upto;
+  __syncthreads();
+  for (int w = 0; w < wave; ++w) upto += wave_total[w];
+  if (tid < experts) {
+    int row = upto - sum;
+    if (tid == 0) offsets[0] = 0;
+    offsets[tid + 1] = upto;
+    for (int w = 0; w < 16; ++w) {
+      const int n = count[w][tid];
+      count[w][tid] = row;
+      row += n;
+    }
+  }
+  int used = 0;
+  for (int w = 0; w < 16; ++w) used += wave_total[w];
+  __syncthreads();
+  walk_chunk<true>(ids, lo, hi, experts, bits, count[wave], positions, slot_of);
+  for (int i = used + tid; i < slots; i += 1024) slot_of[i] = -1;
+}
+constexpr int64_t kSmallRoute = 8192;  // one kernel 7 us against three kernels' 8 and their launches' 18 at 192 slots
+
 struct RoutePlan {
   int64_t chunk;
   int chunks;
@@ -126,7 +170,7 @@ template <typename T, int V>
 __global__ __launch_bounds__(256) void dispatch_kernel(const T* x, int64_t ldx, const int32_t* slots, int64_t count,
                                                        int choices, int64_t width, T* rows, int64_t ldr) {
   using P = Pack<T, V>;
-  const int64_t i = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6);
+  const int64_t i = (int64_t(blockIdx.y) * gridDim.x + blockIdx.x) * 4 + (threadIdx.x >> 6);
   if (i >= count) return;
   const int slot = slots[i];
   const bool here = slot >= 0 && slot < count;
@@ -142,8 +186,8 @@ __global__ __launch_bounds__(256) void combine_kernel(const T* h, int64_t ldh, c
                                                       const float* gates, int64_t tokens, int choices, int64_t width,
                                                       T* out, int64_t ldo) {
   using P = Pack<T, V>;
-  const int64_t t = int64_t(blockIdx.x) * blockDim.y + threadIdx.y;
-  const int64_t c = int64_t(blockIdx.y) * blockDim.x + threadIdx.x;
+  const int64_t t = (int64_t(blockIdx.y) * gridDim.x + blockIdx.x) * blockDim.y + threadIdx.y;
+  const int64_t c = int64_t(blockIdx.z) * blockDim.x + threadIdx.x;
   if (t >= tokens || c >= width / V) return;
   const int64_t count = tokens * choices;
   float sum[V] = {};
@@ -161,48 +205,90 @@ __global__ __launch_bounds__(256) void combine_kernel(const T* h, int64_t ldh, c
   reinterpret_cast<P*>(out + t * ldo)[c] = o;
 }
 
-// One wave per row: it scales dout's row into dh and sums its product with h's row.
-template <typename T, int V>
+// One wave per token: dout's row is read once and stays in registers (Held packs per lane;
+// longer rows take several rounds), then for each choice h's row is read, its product with
+// dout summed and dh's row written. The blocks behind the tokens' look for rows that no
+// slot has and clear them.
+template <typename T, int V, int Held>
 __global__ __launch_bounds__(256) void combine_backward_kernel(const T* dout, int64_t ldo, const T* h, int64_t ldh,
                                                                const int32_t* positions, const int32_t* slots,
-                                                               const float* gates, int64_t count, int choices,
+                                                               const float* gates, int64_t tokens, int choices,
                                                                int64_t width, T* dh, int64_t lddh, float* dgates) {
   using P = Pack<T, V>;
-  const int64_t i = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6);
-  if (i >= count) return;
-  const int lane = threadIdx.x & 63;
-  const int slot = slots[i];
-  const bool here = slot >= 0 && slot < count;
-  const float gate = here && gates ? gates[slot] : 1.0f;
-  const P* src = reinterpret_cast<const P*>(dout + (here ? slot / choices : 0) * ldo);
-  const P* hrow = reinterpret_cast<const P*>(h + i * ldh);
-  P* dst = reinterpret_cast<P*>(dh + i * lddh);
-  float sum = 0.0f;
-  const int64_t n = width / V;
-  const P zero = {};
-  for (int64_t c = lane; c < n; c += 64) {
-    const P d = here ? src[c] : zero;
-    if (dgates && here) {
-      const P v = hrow[c];
-#pragma unroll
-      for (int q = 0; q < V; ++q) sum += widen(d.v[q]) * widen(v.v[q]);
+  const int64_t count = tokens * choices, n = width / V, token_blocks = (tokens + 3) / 4;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t block = int64_t(blockIdx.y) * gridDim.x + blockIdx.x;
+  if (block >= token_blocks) {
+    if (!dh) return;
+    const int64_t first = (block - token_blocks) * 256 + wave * 64;
+    const int slot = first + lane < count ? slots[first + lane] : 0;
+    unsigned long long empty = __ballot(slot < 0 || slot >= count);
+    const P zero = {};
+    while (empty) {
+      const int l = __ffsll(empty) - 1;
+      empty &= empty - 1;
+      P* dst = reinterpret_cast<P*>(dh + (first + l) * lddh);
+      for (int64_t c = lane; c < n; c += 64) dst[c] = zero;
     }
-    if (dh) {
-      P o;
-#pragma unroll
-      for (int q = 0; q < V; ++q) o.v[q] = narrow<T>(gate * widen(d.v[q]));
-      dst[c] = here ? o : zero;
-    }
+    return;
   }
-  if (dgates) {
+  const int64_t t = block * 4 + wave;
+  if (t >= tokens) return;
+  const P* src = reinterpret_cast<const P*>(dout + t * ldo);
+  for (int j0 = 0; j0 < choices; j0 += 64) {  // lanes hold the choices' rows, gates and sums
+    const bool mine = j0 + lane < choices;
+    const int64_t at = t * choices + j0 + lane;
+    int row = mine ? positions[at] : -1;
+    if (row >= count) row = -1;
+    const float gate = mine && row >= 0 && gates ? gates[at] : 1.0f;
+    float dot = 0.0f;
+    const int here = min(64, choices - j0);
+    for (int64_t c0 = 0; c0 < n; c0 += 64 * Held) {
+      P d[Held];
 #pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) sum += __shfl_xor(sum, d);
-    if (lane == 0) {
-      if (here) dgates[slot] = sum;
-      const int p = positions[i];  // of the slot with this row's number
-      if (p < 0 || p >= count) dgates[i] = 0.0f;
+      for (int i = 0; i < Held; ++i)
+        if (c0 + i * 64 + lane < n) d[i] = src[c0 + i * 64 + lane];
+      for (int j = 0; j < here; ++j) {
+        const int r = __builtin_amdgcn_readlane(row, j);
+        if (r < 0) continue;
+        const float scale = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(gate), j));
+        float sum = 0.0f;
+        if (dgates) {
+          const P* hrow = reinterpret_cast<const P*>(h + r * ldh);
+          P v[Held];
+#pragma unroll
+          for (int i = 0; i < Held; ++i)
+            if (c0 + i * 64 + lane < n) v[i] = hrow[c0 + i * 64 + lane];
+#pragma unroll
+          for (int i = 0; i < Held; ++i)
+            if (c0 + i * 64 + lane < n)
+#pragma unroll
+              for (int q = 0; q < V; ++q) sum += widen(d[i].v[q]) * widen(v[i].v[q]);
+#pragma unroll
+          for (int k = 32; k >= 1; k >>= 1) sum += __shfl_xor(sum, k);
+          if (lane == j) dot += sum;
+        }
+        if (dh) {
+          P* dst = reinterpret_cast<P*>(dh + r * lddh);
+#pragma unroll
+          for (int i = 0; i < Held; ++i)
+            if (c0 + i * 64 + lane < n) {
+              P o;
+#pragma unroll
+              for (int q = 0; q < V; ++q) o.v[q] = narrow<T>(scale * widen(d[i].v[q]));
+              dst[c0 + i * 64 + lane] = o;
+            }
+        }
+      }
     }
+    if (mine && dgates) dgates[at] = dot;
   }
+}
+
+// A grid of n workgroups: one dimension holds less than 2^32 threads.
+inline dim3 flat_grid(int64_t n) {
+  const int64_t x = std::min<int64_t>(n, 1 << 20);
+  return dim3(unsigned(x), unsigned((n + x - 1) / x));
 }
 
 // Whether rows of `width` elements at base p, ld apart, are whole 16-byte vectors.
@@ -215,7 +301,9 @@ inline bool on_grid(const void* p, int64_t ld, int64_t width, int size) {
 
 using namespace prod;
 
-int64_t route_workspace(int64_t slots, int experts) { return int64_t(route_plan(slots).chunks) * experts * 4; }
+int64_t route_workspace(int64_t slots, int experts) {
+  return slots <= kSmallRoute ? 0 : int64_t(route_plan(slots).chunks) * experts * 4;
+}
 
 int launch_route(const int32_t* ids, int64_t slots, int experts, int32_t* offsets, int32_t* positions, int32_t* slot_of,
                  void* workspace, void* stream, std::string* err) {
@@ -223,13 +311,16 @@ int launch_route(const int32_t* ids, int64_t slots, int experts, int32_t* offset
   const RoutePlan p = route_plan(slots);
   int bits = 1;
   while ((1 << bits) <= experts) ++bits;
+  if (slots <= kSmallRoute) {
+    hipLaunchKernelGGL(route_small_kernel, dim3(1), dim3(1024), 0, s, ids, int(slots), experts, bits, offsets, positions,
+                       slot_of);
+    return hip_status("route launch", err);
+  }
   int32_t* counts = static_cast<int32_t*>(workspace);
-  if (p.chunks)
-    hipLaunchKernelGGL(route_count_kernel, dim3(p.chunks), dim3(64), 0, s, ids, slots, p.chunk, experts, bits, counts);
+  hipLaunchKernelGGL(route_count_kernel, dim3(p.chunks), dim3(64), 0, s, ids, slots, p.chunk, experts, bits, counts);
   hipLaunchKernelGGL(route_scan_kernel, dim3(1), dim3(kMaxExperts), 0, s, counts, p.chunks, experts, offsets);
-  if (p.chunks)
-    hipLaunchKernelGGL(route_place_kernel, dim3(p.chunks), dim3(64), 0, s, ids, slots, p.chunk, experts, bits, counts,
-                       offsets, positions, slot_of);
+  hipLaunchKernelGGL(route_place_kernel, dim3(p.chunks), dim3(64), 0, s, ids, slots, p.chunk, experts, bits, counts,
+                     offsets, positions, slot_of);
   return hip_status("route launch", err);
 }
 
@@ -238,7 +329,7 @@ static int dispatch_t(const void* x, int64_t ldx, const int32_t* slots, int64_t 
                       void* rows, int64_t ldr, hipStream_t s, std::string* err) {
   constexpr int V = 16 / int(sizeof(T));
   const int64_t count = tokens * choices;
-  const dim3 grid(unsigned((count + 3) / 4));
+  const dim3 grid = flat_grid((count + 3) / 4);
   auto go = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, static_cast<const T*>(x), ldx, slots, count, choices, width,
                        static_cast<T*>(rows), ldr);
@@ -264,7 +355,8 @@ static int combine_t(const void* h, int64_t ldh, const int32_t* positions, const
   int bx = 64;  // whole waves along a row; short rows share a workgroup
   while (bx < 256 && bx < n) bx *= 2;
   const dim3 block(bx, 256 / bx);
-  const dim3 grid(unsigned((tokens + block.y - 1) / block.y), unsigned((n + bx - 1) / bx));
+  dim3 grid = flat_grid((tokens + block.y - 1) / block.y);
+  grid.z = unsigned((n + bx - 1) / bx);
   auto go = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, grid, block, 0, s, static_cast<const T*>(h), ldh, positions, gates, tokens, choices,
                        width, static_cast<T*>(out), ldo);
@@ -286,16 +378,15 @@ static int combine_backward_t(const void* dout, int64_t ldo, const void* h, int6
                               const int32_t* slots, const float* gates, int64_t tokens, int choices, int64_t width,
                               void* dh, int64_t lddh, float* dgates, hipStream_t s, std::string* err) {
   constexpr int V = 16 / int(sizeof(T));
-  const int64_t count = tokens * choices;
-  const dim3 grid(unsigned((count + 3) / 4));
+  const dim3 grid = flat_grid((tokens + 3) / 4 + (tokens * choices + 255) / 256);
   auto go = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, static_cast<const T*>(dout), ldo, static_cast<const T*>(h), ldh,
-                       positions, slots, gates, count, choices, width, static_cast<T*>(dh), lddh, dgates);
+                       positions, slots, gates, tokens, choices, width, static_cast<T*>(dh), lddh, dgates);
   };
   const bool wide = on_grid(dout, ldo, width, sizeof(T)) && (!dgates || on_grid(h, ldh, width, sizeof(T))) &&
                     (!dh || on_grid(dh, lddh, width, sizeof(T)));
-  if (wide) go(combine_backward_kernel<T, V>);
-  else go(combine_backward_kernel<T, 1>);
+  if (wide) go(combine_backward_kernel<T, V, 8>);
+  else go(combine_backward_kernel<T, 1, 8>);
   return hip_status("combine gradient launch", err);
 }
 

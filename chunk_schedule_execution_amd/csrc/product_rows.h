@@ -104,7 +104,7 @@ __device__ inline void product_rows(const ProductArgs& g, int slabs) {
     const int64_t at = t.row + r, n = col + c;
     if (at >= t.end || n >= g.n) continue;
     const float z = nothing ? 0.0f : (sums[0][r][c] + sums[1][r][c]) + (sums[2][r][c] + sums[3][r][c]);
-    if (g.partial) g.partial[(int64_t(blockIdx.y) * g.m + at) * g.n + n] = z;
+    if (g.partial) *partial_at(g, blockIdx.y, at, n) = z;
     else finish_one<T>(g, z, at, n, t.group, nothing);
   }
 }

@@ -193,8 +193,12 @@ __device__ inline void product_tile(const ProductArgs& g, ProductMode mode, int 
   const T* A = static_cast<const T*>(g.a);
   const T* B = static_cast<const T*>(g.b);
   T* C = static_cast<T*>(g.c);
+  // groups leave some of the grid without a tile: only those that exist are spread over
+  // the XCDs
+  const unsigned tiles = mode == kRaggedM ? unsigned(count_tiles(g.offsets, g.groups, g.m, BM, true)) * tiles_n : gridDim.x;
+  if (blockIdx.x >= tiles) return;
   int band, column;
-  place_tile(blockIdx.x, gridDim.x, tiles_n, band, column);
+  place_tile(blockIdx.x, tiles, tiles_n, band, column);
   const int64_t col = int64_t(column) * BN;
   int group = 0;
   int64_t row = 0, m_end = g.m, k_lo = 0, k_hi = g.k;
@@ -242,8 +246,8 @@ __device__ inline void product_tile(const ProductArgs& g, ProductMode mode, int 
     // to arrive; the rows still to be multiplied cover the barrier and the first reads.
     // Loads behind the end give zeros and nothing multiplies them, so no step branches.
     typedef decltype(ra.read(a0, 0, 0)) vec;
-    constexpr int Rows = 2 * FM, Ahead = 4, Ring = 8;
-    static_assert(Ahead <= FM && Rows % Ring == 0, "a ring of fragments");
+    constexpr int Rows = 2 * FM, Ahead = FM < 4 ? FM : 4, Ring = 2 * Ahead;
+    static_assert(Rows % Ring == 0, "a ring of fragments");
     vec fa[Ring], fb[2][FN];
     auto read_a = [&](const T* la, int r) { fa[r % Ring] = ra.read(la, r % FM, r / FM % 2); };
     auto read_b = [&](const T* lb, int h) {
@@ -301,16 +305,9 @@ __device__ inline void product_tile(const ProductArgs& g, ProductMode mode, int 
   constexpr int kStage = 1;                              // fragments of rows per stage
   float* const stage = reinterpret_cast<float*>(a0) + wave * (kStage * 16 * WTN);
   static_assert(kStage * 16 * WTN * 4 * WM * WN <= BM * 128, "the waves' stages fit");
-  const T* bias = g.bias && !nothing ? static_cast<const T*>(g.bias) + group * g.bias_stride : nullptr;
-  const T* residual = static_cast<const T*>(g.residual);
-  T* preact = static_cast<T*>(g.preact);
   const int64_t c = col + wn + (lane % kLanesPerRow) * 8;
   const int n = int(min(int64_t(8), g.n - c));
-  const bool vec_c = g.ldc * sizeof(T) % 16 == 0 && reinterpret_cast<uintptr_t>(C) % 16 == 0;
-  const bool vec_r = g.ldr * sizeof(T) % 16 == 0 && reinterpret_cast<uintptr_t>(residual) % 16 == 0;
-  const bool vec_p = g.ldp * sizeof(T) % 16 == 0 && reinterpret_cast<uintptr_t>(preact) % 16 == 0;
-  float bv[8] = {};
-  if (bias && n > 0) load8(bias + c, false, n, bv);
+  const Finish<T> finish(g, C, c, n, group, nothing);
 #pragma unroll
   for (int i0 = 0; i0 < FM; i0 += kStage) {
 #pragma unroll
@@ -330,21 +327,8 @@ __device__ inline void product_tile(const ProductArgs& g, ProductMode mode, int 
       *reinterpret_cast<f32x4*>(v) = *reinterpret_cast<const f32x4*>(stage + r * WTN + ((chunk ^ r) % kChunks) * 4);
       *reinterpret_cast<f32x4*>(v + 4) =
           *reinterpret_cast<const f32x4*>(stage + r * WTN + (((chunk + 1) ^ r) % kChunks) * 4);
-      if (g.partial) {
-        store8(g.partial + (int64_t(blockIdx.y) * g.m + at) * g.n + c, g.n % 4 == 0, n, v);
-        continue;
-      }
-#pragma unroll
-      for (int q = 0; q < 8; ++q) v[q] += bv[q];
-      if (preact) store8(preact + at * g.ldp + c, vec_p, n, v);
-      if (!nothing) act8(v, g.act);
-      if (residual) {
-        float w[8];
-        load8(residual + at * g.ldr + c, vec_r, n, w);
-#pragma unroll
-        for (int q = 0; q < 8; ++q) v[q] += w[q];
-      }
-      store8(C + at * g.ldc + c, vec_c, n, v);
+      if (g.partial) store8(partial_at(g, blockIdx.y, at, c), true, n, v);
+      else finish.row(at, v);
     }
     __builtin_amdgcn_wave_barrier();
   }

@@ -120,7 +120,7 @@ BackwardPlan backward_plan(const ccl_linear_desc& d, bool grouped) {
   s.own_dz = d.activation != CCL_ACT_NONE || grid_of(d) == kOffGrid || d.ld_out * size % 16 || padded != d.out_features;
   s.ld_dz = s.own_dz ? padded : d.ld_out;
   s.at_partial = s.own_dz ? align16(d.rows * padded * size) : 0;
-  s.at_product = s.at_partial + align16(slope_tiles(d.rows, grouped ? d.experts : 0) * d.out_features * 4);
+  s.at_product = s.at_partial + align16(slope_tiles(d.rows, d.out_features, grouped ? d.experts : 0) * d.out_features * 4);
   const OperandGrid dz = s.own_dz ? kPadded : kByStrides;
   s.dx = plan_product(d.dtype, false, true, grouped ? kRaggedM : kPlain, dx_args(d, s.ld_dz), dz, grid_of(d));
   s.dw = plan_product(d.dtype, true, true, grouped ? kRaggedK : kPlain, dw_args(d, s.ld_dz), dz, grid_of(d));

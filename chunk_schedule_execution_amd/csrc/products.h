@@ -31,11 +31,15 @@ struct ProductArgs {
   void* preact = nullptr;
   int64_t ldr = 0, ldp = 0;
   int act = 0;
-  float* partial = nullptr;  // set: the splits' fp32 sums go here, [split][m][n], and nothing else happens
+  float* partial = nullptr;  // set: the splits' fp32 sums go here, [split][m][partial_ld(n)], and nothing else happens
 };
+#ifdef __HIPCC__
+__host__ __device__
+#endif
+inline int64_t partial_ld(int64_t n) { return (n + 3) / 4 * 4; }
 
 // How a product is run, from its sizes alone.
-enum ProductKind : int { kRows16, kRows32, kRows64, kTile128, kTile256 };
+enum ProductKind : int { kRows16, kRows32, kRows64, kTile64, kTile128, kTile256 };
 struct ProductPlan {
   ProductKind kind = kTile128;
   int columns = 1;                   // few-row kinds: 16-column fragments per workgroup
@@ -67,7 +71,7 @@ struct SlopeArgs {
   int groups = 1;
   int act = 0;
 };
-int64_t slope_tiles(int64_t rows, int groups);  // groups: 0 without offsets
+int64_t slope_tiles(int64_t rows, int64_t n, int groups);  // groups: 0 without offsets
 int launch_slope(int dtype, const SlopeArgs& args, void* stream, std::string* err);
 
 int64_t route_workspace(int64_t slots, int experts);

@@ -1,6 +1,7 @@
 // Products beside the collectives for gfx950: C = act(A B^T + bias) + residual, plain or
 // grouped by expert with ragged sizes, for the forward pass and both gradients.
 #include <algorithm>
+#include <cmath>
 
 #include "products_device.h"
 
@@ -52,27 +53,39 @@ int regrid(int dtype, const void* src, int64_t ld, int64_t rows, int64_t len, vo
 }
 
 // ---- joining the splits of the summed dimension -------------------------------------------
+// A workgroup takes 16 rows of a group by 256 columns, 8 columns per thread, and adds the
+// splits in order.
 constexpr int kJoinRows = 16;
 
 template <typename T>
-__global__ __launch_bounds__(256) void join_kernel(ProductArgs g, const float* partial, int splits) {
+__global__ __launch_bounds__(256) void join_kernel(ProductArgs g, int splits) {
   const RowTile t = find_tile(g.offsets, g.groups, g.m, kJoinRows, blockIdx.x, true);
-  const int64_t c = int64_t(blockIdx.y) * 256 + threadIdx.x;
+  const int64_t c = int64_t(blockIdx.y) * 256 + (threadIdx.x & 31) * 8;
   if (t.group < 0 || c >= g.n) return;
   const bool nothing = g.offsets && t.group == g.groups;
   const int64_t end = min(t.end, t.row + kJoinRows);
-  for (int64_t r = t.row; r < end; ++r) {
-    float z = 0.0f;
-    if (!nothing)
-      for (int s = 0; s < splits; ++s) z += partial[(int64_t(s) * g.m + r) * g.n + c];
-    finish_one<T>(g, z, r, c, t.group, nothing);
+  const int n = int(min(int64_t(8), g.n - c));
+  const Finish<T> finish(g, static_cast<T*>(g.c), c, n, t.group, nothing);
+#pragma unroll 2
+  for (int64_t r = t.row + (threadIdx.x >> 5); r < end; r += 8) {
+    float z[8] = {};
+    if (!nothing) {
+#pragma unroll 4
+      for (int s = 0; s < splits; ++s) {
+        float v[8];
+        load8(partial_at(g, s, r, c), true, n, v);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) z[q] += v[q];
+      }
+    }
+    finish.row(r, z);
   }
 }
 
-int join(int dtype, const ProductArgs& g, const float* partial, int splits, hipStream_t s, std::string* err) {
+int join(int dtype, const ProductArgs& g, int splits, hipStream_t s, std::string* err) {
   const dim3 grid(unsigned((g.m + kJoinRows - 1) / kJoinRows + (g.offsets ? g.groups : 0)), unsigned((g.n + 255) / 256));
-  if (dtype == CCL_BF16) hipLaunchKernelGGL(join_kernel<bf16>, grid, dim3(256), 0, s, g, partial, splits);
-  else hipLaunchKernelGGL(join_kernel<float>, grid, dim3(256), 0, s, g, partial, splits);
+  if (dtype == CCL_BF16) hipLaunchKernelGGL(join_kernel<bf16>, grid, dim3(256), 0, s, g, splits);
+  else hipLaunchKernelGGL(join_kernel<float>, grid, dim3(256), 0, s, g, splits);
   return hip_status("join launch", err);
 }
 
@@ -83,7 +96,12 @@ int join(int dtype, const ProductArgs& g, const float* partial, int splits, hipS
 // the order in which workgroups run. Bound by memory.
 constexpr int kSlopeLanes = 8;  // rows that a workgroup has in hand at a time
 
-int slope_height(int64_t rows) { return rows < (int64_t(1) << 26) ? 64 : 4096; }
+// Rows of a tile: 64, fewer where those would not fill the chip, more where a grid could
+// not hold the tiles.
+int slope_height(int64_t rows, int64_t n) {
+  if (rows >= int64_t(1) << 26) return 4096;
+  return rows / 64 * ((n + 255) / 256) < 1024 ? 16 : 64;
+}
 
 template <typename T>
 __global__ __launch_bounds__(256) void slope_kernel(SlopeArgs g, int height, bool vec_o, bool vec_p) {
@@ -150,13 +168,13 @@ __global__ __launch_bounds__(256) void bias_sum_kernel(SlopeArgs g, int height) 
 
 template <typename T>
 int slope_t(const SlopeArgs& g, hipStream_t s, std::string* err) {
-  const int height = slope_height(g.rows);
+  const int height = slope_height(g.rows, g.n);
   auto grid16 = [](const void* p, int64_t ld) {
     return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * sizeof(T) % 16 == 0;
   };
   if (g.rows > 0 && (g.dz || g.dbias))
     hipLaunchKernelGGL(slope_kernel<T>,
-                       dim3(unsigned(slope_tiles(g.rows, g.offsets ? g.groups : 0)), unsigned((std::max(g.n, g.ldz) + 255) / 256)),
+                       dim3(unsigned(slope_tiles(g.rows, g.n, g.offsets ? g.groups : 0)), unsigned((std::max(g.n, g.ldz) + 255) / 256)),
                        dim3(256), 0, s, g, height, grid16(g.dout, g.ldo), grid16(g.preact, g.ldp));
   if (g.dbias)
     hipLaunchKernelGGL(bias_sum_kernel<T>, dim3(unsigned((g.n + 63) / 64), unsigned(g.groups)), dim3(256), 0, s, g, height);
@@ -166,8 +184,8 @@ int slope_t(const SlopeArgs& g, hipStream_t s, std::string* err) {
 }  // namespace
 }  // namespace prod
 
-int64_t slope_tiles(int64_t rows, int groups) {
-  const int height = prod::slope_height(rows);
+int64_t slope_tiles(int64_t rows, int64_t n, int groups) {
+  const int height = prod::slope_height(rows, n);
   return (rows + height - 1) / height + groups;
 }
 
@@ -175,6 +193,63 @@ int launch_slope(int dtype, const SlopeArgs& args, void* stream, std::string* er
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   return dtype == CCL_BF16 ? prod::slope_t<prod::bf16>(args, s, err) : prod::slope_t<float>(args, s, err);
 }
+
+namespace {
+
+// The tile size and the number of splits that should take least time. A workgroup's step
+// (128 bytes of the summed dimension) takes, by the number of workgroups on its compute
+// unit at a time, measured at 1024^2, 2048^2 and 4096^2 by 4096 (us):
+//             alone   more of them                  start and end of a tile
+//   bf16  64   0.41   0.68 for 4                    4
+//   bf16 128   0.62   0.98 for 2                    5
+//   bf16 256   1.40   (its LDS fills the unit)      10
+//   fp32  64   0.60   0.50 each                     4
+//   fp32 128   1.90   1.90 each                     5
+// fp32 is bound by the matrix instructions in either size; in bf16 a larger tile reads
+// less per product but leaves units idle: 2048^2 x 4096 takes 47 us in 64s or 128s and
+// 87 in 256s, 4096^2 x 4096 189, 130 and 112. Splits cost a second kernel (5 us) and the
+// partial sums' way through memory (written and read at 3.5 TB/s): 512^2 x 4096 takes 31 us
+// unsplit and 17 in 4 splits of 64s, 1024^2 x 1024 11 and 16 in 2.
+void choose_tile(int dtype, ProductMode mode, const ProductArgs& g, ProductPlan& p) {
+  struct Size {
+    ProductKind kind;
+    int edge, resident;
+    double alone, full, ends;
+  };
+  static constexpr Size kBf16[] = {{kTile64, 64, 4, 0.41, 0.68, 4}, {kTile128, 128, 2, 0.62, 0.98, 5}, {kTile256, 256, 1, 1.4, 1.4, 10}};
+  static constexpr Size kF32[] = {{kTile64, 64, 4, 0.60, 2.0, 4}, {kTile128, 128, 2, 1.9, 3.8, 5}};
+  const Size* sizes = dtype == CCL_BF16 ? kBf16 : kF32;
+  const int count = dtype == CCL_BF16 ? 3 : 2;
+  auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
+  constexpr int64_t kUnits = 256;
+  const double summed = double(mode == kRaggedK ? g.k / std::max(1, g.groups) : g.k);
+  const double steps = std::max(1.0, std::ceil(summed * (dtype == CCL_BF16 ? 2 : 4) / 128));
+  double best = 0;
+  for (int i = 0; i < count; ++i) {
+    const Size& z = sizes[i];
+    // groups of rows end in half a tile on average
+    const double bands = mode == kRaggedM && g.groups > 1 ? double(g.m) / z.edge + 0.5 * std::min<int64_t>(g.groups, g.m)
+                                                          : double(up(g.m, z.edge));
+    const double tiles = std::max(1.0, bands) * double(up(g.n, z.edge)) * (mode == kRaggedK ? g.groups : 1);
+    if (tiles > (1 << 22)) continue;
+    for (int splits : {1, 2, 3, 4, 6, 8, 12, 16}) {
+      if (splits > 1 && (mode == kRaggedK || steps < 4 * splits)) break;
+      const int64_t each = int64_t(std::ceil(tiles * splits / kUnits));  // workgroups per compute unit
+      auto step = [&](int64_t n) { return z.resident == 1 || n <= 1 ? z.alone * n : z.alone + (z.full - z.alone) * (n - 1) / (z.resident - 1); };
+      const double rounds = double(each / z.resident);
+      double us = std::ceil(steps / splits) * (rounds * step(z.resident) + step(each % z.resident)) + z.ends * (rounds + (each % z.resident != 0));
+      if (splits > 1) us += 5 + 2.0 * splits * double(g.m) * double(g.n) * 4 / 3.5e6;
+      if (best == 0 || us < best) {
+        best = us;
+        p.kind = z.kind;
+        p.splits = splits;
+      }
+    }
+  }
+  if (best == 0) p.kind = sizes[count - 1].kind;
+}
+
+}  // namespace
 
 ProductPlan plan_product(int dtype, bool a_by_k, bool b_by_k, ProductMode mode, const ProductArgs& g,
                          OperandGrid a_grid, OperandGrid b_grid) {
@@ -188,7 +263,8 @@ ProductPlan plan_product(int dtype, bool a_by_k, bool b_by_k, ProductMode mode, 
   const int64_t mean = g.m / g.groups;
   if (!a_by_k && !b_by_k && mode != kRaggedK && mean <= 48 && g.m <= 64 * int64_t(g.groups) &&
       up(g.m, 16) * up(g.n, 16) < (1 << 23)) {
-    p.kind = mean <= 12 && (g.groups > 1 || g.m <= 16) ? kRows16 : mean <= 24 && (g.groups > 1 || g.m <= 32) ? kRows32 : kRows64;
+    if (g.groups == 1) p.kind = g.m <= 16 ? kRows16 : g.m <= 32 ? kRows32 : kRows64;
+    else p.kind = mean <= 8 ? kRows16 : mean <= 20 ? kRows32 : kRows64;
     p.vec = on_a && on_b;
     const int64_t height = p.kind == kRows16 ? 16 : p.kind == kRows32 ? 32 : 64;
     const int64_t bands = up(g.m, height) + (g.groups > 1 ? std::min<int64_t>(g.groups, g.m) : 0);
@@ -196,14 +272,7 @@ ProductPlan plan_product(int dtype, bool a_by_k, bool b_by_k, ProductMode mode, 
     const int64_t wgs = std::max<int64_t>(1, bands * up(g.n, 16 * p.columns));
     p.splits = int(std::max<int64_t>(1, std::min<int64_t>(512 / wgs, g.k * size / 4096)));
   } else {
-    const int64_t groups = mode == kRaggedK ? g.groups : 1;
-    const int64_t rows = mode == kRaggedM ? g.m / g.groups : g.m;  // of one group, on average
-    const int64_t big = up(g.m, 256) * up(g.n, 256) * groups;
-    p.kind = dtype == CCL_BF16 && big >= 200 && rows >= 192 ? kTile256 : kTile128;
-    const int64_t tiles = std::max<int64_t>(
-        1, p.kind == kTile256 ? big : (up(g.m, 128) + (mode == kRaggedM ? g.groups / 2 : 0)) * up(g.n, 128) * groups);
-    const int64_t steps = up(g.k, 128 / size);
-    if (mode != kRaggedK && tiles < 192) p.splits = int(std::max<int64_t>(1, std::min({up(384, tiles), steps / 4, int64_t(16)})));
+    choose_tile(dtype, mode, g, p);
     p.copy_a = !on_a;
     p.copy_b = !on_b;
     p.ld_a = up(a_by_k ? g.m : g.k, v) * v;
@@ -214,7 +283,7 @@ ProductPlan plan_product(int dtype, bool a_by_k, bool b_by_k, ProductMode mode, 
   const int64_t rows_b = (b_by_k ? g.k : g.n) * (mode == kRaggedM ? g.groups : 1);
   p.at_b = p.copy_a ? up(rows_a * p.ld_a * size, 16) * 16 : 0;
   p.at_partial = p.at_b + (p.copy_b ? up(rows_b * p.ld_b * size, 16) * 16 : 0);
-  p.bytes = p.at_partial + (p.splits > 1 ? p.splits * g.m * g.n * 4 : 0);
+  p.bytes = p.at_partial + (p.splits > 1 ? p.splits * g.m * partial_ld(g.n) * 4 : 0);
   return p;
 }
 
@@ -239,11 +308,11 @@ int launch_product(int dtype, bool a_by_k, bool b_by_k, ProductMode mode, const 
   }
   if (plan.splits > 1) g.partial = reinterpret_cast<float*>(ws + plan.at_partial);
   int rc;
-  if (plan.kind == kRows16 || plan.kind == kRows32 || plan.kind == kRows64) rc = launch_rows(dtype, g, plan, s, err);
+  if (plan.kind <= kRows64) rc = launch_rows(dtype, g, plan, s, err);
   else if (dtype == CCL_BF16) rc = launch_tile_bf16(a_by_k, b_by_k, mode, g, plan, s, err);
   else rc = launch_tile_f32(a_by_k, b_by_k, mode, g, plan, s, err);
   if (rc || plan.splits == 1) return rc;
-  return join(dtype, g, g.partial, plan.splits, s, err);
+  return join(dtype, g, plan.splits, s, err);
 }
 
 }  // namespace ccl

@@ -151,6 +151,31 @@ __device__ inline void group_bounds(const int32_t* offsets, int64_t rows, int gr
   hi = max(top, min(offsets[group + 1], int(rows)));
 }
 
+// How many tiles find_tile knows.
+__device__ inline int count_tiles(const int32_t* offsets, int groups, int64_t rows, int height, bool with_rest) {
+  if (offsets == nullptr) return int((rows + height - 1) / height);
+  const int lane = threadIdx.x & 63, last = with_rest ? groups : groups - 1;
+  int total = 0, carry_max = 0;
+  for (int base = 0; base <= last; base += 64) {
+    const int e = base + lane;
+    int hi = e < groups ? max(0, min(offsets[e + 1], int(rows))) : int(rows);
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int v = __shfl_up(hi, d);
+      if (lane >= d) hi = max(hi, v);
+    }
+    hi = max(hi, carry_max);
+    int lo = __shfl_up(hi, 1);
+    if (lane == 0) lo = carry_max;
+    int tiles = e <= last ? int((int64_t(hi) - lo + height - 1) / height) : 0;
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) tiles += __shfl_xor(tiles, d);
+    total += uniform(tiles);
+    carry_max = __builtin_amdgcn_readlane(hi, 63);
+  }
+  return total;
+}
+
 // The numbers of a group's tiles of `height` rows, [first, last).
 __device__ inline void group_tiles(const int32_t* offsets, int groups, int64_t rows, int height, int group,
                                    int64_t& first, int64_t& last) {
@@ -257,7 +282,50 @@ __device__ inline void slope8(float* v, const float* z, int act) {
 #undef CCL_SLOPE8
 }
 
-// bias, activation, residual and stores of one result z of column c.
+template <typename T>
+__device__ inline bool on_vectors(const void* p, int64_t ld) {
+  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * sizeof(T) % 16 == 0;
+}
+
+// Bias, activation, residual and stores of results, 8 columns (c .. c + n - 1, n <= 8) of a
+// row at a time.
+template <typename T>
+struct Finish {
+  const T* residual;
+  T* preact;
+  T* out;
+  int64_t ldr, ldp, ldc, c;
+  float bias[8];
+  int n, act;
+  bool vec_c, vec_r, vec_p, nothing;
+
+  // nothing: rows of no group, whose results are zeros (z has to be 0)
+  __device__ inline Finish(const ProductArgs& g, T* to, int64_t column, int count, int group, bool none)
+      : residual(static_cast<const T*>(g.residual)), preact(static_cast<T*>(g.preact)), out(to), ldr(g.ldr),
+        ldp(g.ldp), ldc(g.ldc), c(column), n(count), act(none ? CCL_ACT_NONE : g.act), nothing(none) {
+    vec_c = on_vectors<T>(out, ldc);
+    vec_r = on_vectors<T>(residual, ldr);
+    vec_p = on_vectors<T>(preact, ldp);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) bias[q] = 0.0f;
+    if (g.bias && !none && n > 0) load8(static_cast<const T*>(g.bias) + group * g.bias_stride + c, false, n, bias);
+  }
+  __device__ inline void row(int64_t r, float* z) const {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) z[q] += bias[q];
+    if (preact) store8(preact + r * ldp + c, vec_p, n, z);
+    act8(z, act);
+    if (residual) {
+      float w[8];
+      load8(residual + r * ldr + c, vec_r, n, w);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) z[q] += w[q];
+    }
+    store8(out + r * ldc + c, vec_c, n, z);
+  }
+};
+
+// The same for a single result.
 template <typename T>
 __device__ inline void finish_one(const ProductArgs& g, float z, int64_t row, int64_t c, int group, bool nothing) {
   float v = 0.0f;
@@ -268,6 +336,11 @@ __device__ inline void finish_one(const ProductArgs& g, float z, int64_t row, in
   if (g.preact) static_cast<T*>(g.preact)[row * g.ldp + c] = narrow<T>(nothing ? 0.0f : z);
   if (g.residual) v += widen(static_cast<const T*>(g.residual)[row * g.ldr + c]);
   static_cast<T*>(g.c)[row * g.ldc + c] = narrow<T>(v);
+}
+
+// Where split `s`'s fp32 sum of a result goes; rows of whole 16-byte vectors.
+__device__ inline float* partial_at(const ProductArgs& g, int s, int64_t row, int64_t c) {
+  return g.partial + (int64_t(s) * g.m + row) * partial_ld(g.n) + c;
 }
 
 }  // namespace prod
