@@ -1,6 +1,8 @@
 // The tiled product kernel for gfx950: operands whose rows lie on the 16-byte grid.
 #pragma once
 
+#include <algorithm>
+
 #include "products_device.h"
 
 namespace ccl {
@@ -35,57 +37,58 @@ struct OperandTile {
   static constexpr int kChunks = ByK ? R / kVec : 8;  // per stored row
   static_assert(kLoads * Threads == R * 8 && kLoads >= 1, "whole loads");
 
-  const char* base;  // first value of the tile at the current step
-  int64_t step_bytes;
-  int64_t records;   // readable bytes from base (by rows), or of the whole rest (by k)
-  int64_t ld_bytes;
+  // All byte counts within a tile are below 2^32: a stride is at most 2^22 values, so 256
+  // rows of bf16 or 128 of fp32 span 2^31 bytes.
+  const char* base;   // first value of the tile at the current step
+  unsigned records;   // readable bytes from base (by rows), or in the last row of k (by k)
+  unsigned ld_bytes;
   int voff[kLoads];
   int kc;  // by rows: first k value of this lane's chunk
 
   // row: first row (or column) of the tile, end: one past the last; k_lo, k_hi: the summed
   // range. The vector around the last value is read whole.
   __device__ inline void init(const T* p, int64_t ld, int64_t row, int64_t end, int64_t k_lo, int64_t k_hi) {
-    const int tid = threadIdx.x;
-    ld_bytes = ld * kSize;
+    const int tid = here(threadIdx.x);
+    ld_bytes = unsigned(ld * kSize);
     if constexpr (ByK) {
       base = reinterpret_cast<const char*>(p + k_lo * ld + row);
-      step_bytes = ld_bytes * kStep;
-      records = (end - row + kVec - 1) / kVec * 16;  // of the last row: whole vectors
+      records = unsigned(min(int64_t(R), end - row) + kVec - 1) / kVec * 16;  // whole vectors
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
         const int q = i * Threads + tid, k = q / kChunks, c = (q % kChunks) ^ swizzle(k);
-        voff[i] = int(k * ld_bytes) + c * 16;
+        voff[i] = int(unsigned(k) * ld_bytes) + c * 16;
       }
     } else {
       base = reinterpret_cast<const char*>(p + row * ld + k_lo);
-      step_bytes = 128;
-      records = (min(int64_t(R), end - row) - 1) * ld_bytes + (k_hi - k_lo + kVec - 1) / kVec * 16;
+      records = unsigned(min(int64_t(R), end - row) - 1) * ld_bytes + unsigned(k_hi - k_lo + kVec - 1) / kVec * 16;
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
         const int q = i * Threads + tid, r = q / 8, c = (q % 8) ^ (r & 7);
-        voff[i] = int(r * ld_bytes) + c * 16;
+        voff[i] = int(unsigned(r) * ld_bytes) + c * 16;
         kc = c * kVec;  // the same for every i: rows differ by multiples of 8
       }
     }
+    base = uniform(base);
+    records = uniform(int(records));
   }
 
   static __device__ inline int swizzle(int k) { return kSize == 2 ? (k & 3) << 1 : ((k >> 2) & 3) << 2; }
 
   // Starts the loads of the step whose `left` summed values remain, into `lds`, and moves
   // on to the next step. Reads out of range (all of them when none remain) give zeros.
-  __device__ inline void load(T* lds, int64_t left) {
+  __device__ inline void load(T* lds, int left) {
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     unsigned to = unsigned((uintptr_t)(lds_ptr)lds) + wave * 1024;
     asm volatile("" : "+s"(to));
-    const int64_t rest = ByK ? (min(int64_t(kStep), left) - 1) * ld_bytes + records : records;
+    const unsigned rest = ByK ? unsigned(min(kStep, left) - 1) * ld_bytes + records : records;
     const __amdgpu_buffer_rsrc_t rsrc =
-        __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base), 0, left > 0 ? int(rest) : 0, 0x00020000);
+        __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base), 0, uniform(left > 0 ? int(rest) : 0), 0x00020000);
     // by rows, the last step: chunks behind the row's end would be the next row's values
     const bool out = !ByK && left < kStep && kc >= left;
 #pragma unroll
     for (int i = 0; i < kLoads; ++i)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_ptr)(uintptr_t)(to + i * Threads * 16), 16, out ? -1 : voff[i], 0, 0, 0);
-    base += step_bytes;
+    base += ByK ? int64_t(ld_bytes) * kStep : 128;
     if (!ByK) records -= 128;
   }
 };
@@ -152,12 +155,12 @@ __device__ inline f32x4 multiply(f32x4 x, f32x4 y, f32x4 acc) {
   return acc;
 }
 
-// Every wave's loads into LDS but its latest Left have arrived, and every wave's reads
-// before this point are done.
-template <int Left>
+// All waves' reads of LDS before this point are done and their loads into LDS have arrived.
 __device__ inline void steps_arrived() {
-  __builtin_amdgcn_s_waitcnt(0x0F70 | (Left & 15) | (Left >> 4) << 14);  // vmcnt
-  __syncthreads();
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0), lgkmcnt(0)
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
 }
 
 // Which tile a workgroup computes. Workgroups go round the 8 XCDs, each with an L2 of its
@@ -177,183 +180,212 @@ __device__ inline void place_tile(unsigned id, unsigned tiles, int tiles_n, int&
 }
 
 // ---- the kernel ---------------------------------------------------------------------------
-// BM x BN values per workgroup, WM x WN waves, each (BM / WM) x (BN / WN) by matrix
-// instructions of 16 x 16. Two LDS buffers, one barrier per step.
-template <typename T, bool AByK, bool BByK, int BM, int BN, int WM, int WN>
-__device__ inline void product_tile(const ProductArgs& g, ProductMode mode, int tiles_m, int tiles_n) {
-  constexpr int Threads = WM * WN * 64, FM = BM / WM / 16, FN = BN / WN / 16;
-  constexpr int kStep = 128 / int(sizeof(T));
-  constexpr int kTile = kStep;  // values per row of a stored tile
-  __shared__ __attribute__((aligned(1024))) T a0[BM * kTile];
-  __shared__ __attribute__((aligned(1024))) T b0[BN * kTile];
-  __shared__ __attribute__((aligned(1024))) T a1[BM * kTile];
-  __shared__ __attribute__((aligned(1024))) T b1[BN * kTile];
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const T* A = static_cast<const T*>(g.a);
-  const T* B = static_cast<const T*>(g.b);
-  T* C = static_cast<T*>(g.c);
-  // groups leave some of the grid without a tile: only those that exist are spread over
-  // the XCDs
-  const unsigned tiles = mode == kRaggedM ? unsigned(count_tiles(g.offsets, g.groups, g.m, BM, true)) * tiles_n : gridDim.x;
-  if (blockIdx.x >= tiles) return;
+// What a workgroup computes next; all of it uniform.
+struct TileJob {
+  int group = 0;         // `groups`: rows of no group
+  bool there = false;    // false: no such tile
+  int row = 0, m_end = 0, col = 0, k_lo = 0, k_hi = 0;  // all below 2^31
+};
+
+template <int BM, int BN, int Step>
+__device__ inline TileJob find_job(const ProductArgs& g, ProductMode mode, unsigned id, unsigned tiles, int tiles_m,
+                                   int tiles_n) {
+  TileJob j;
+  if (id >= tiles) return j;
   int band, column;
-  place_tile(blockIdx.x, tiles, tiles_n, band, column);
-  const int64_t col = int64_t(column) * BN;
-  int group = 0;
+  place_tile(id, tiles, tiles_n, band, column);
   int64_t row = 0, m_end = g.m, k_lo = 0, k_hi = g.k;
   if (mode == kRaggedK) {
-    group = uniform(band / tiles_m);
-    row = int64_t(band - group * tiles_m) * BM;
-    group_bounds(g.offsets, g.k, group, k_lo, k_hi);
-    C += group * g.c_stride;
+    j.group = uniform(band / tiles_m);
+    row = int64_t(band - j.group * tiles_m) * BM;
+    group_bounds(g.offsets, g.k, j.group, k_lo, k_hi);
   } else {
     const RowTile t = find_tile(g.offsets, g.groups, g.m, BM, band, true);
-    if (t.group < 0) return;
-    group = uniform(t.group);
+    j.group = uniform(t.group);
     row = t.row;
     m_end = t.end;
-    if (group == g.groups) k_hi = 0;  // rows of no group: zeros
-    else B += group * g.b_stride;
+    if (mode == kRaggedM && j.group == g.groups) k_hi = 0;  // rows of no group: zeros
   }
-  const bool nothing = mode == kRaggedM && group == g.groups;
-  row = uniform(int(row));  // row counts are below 2^31
-  m_end = uniform(int(m_end));
-  k_lo = uniform(int(k_lo));
-  k_hi = uniform(int(k_hi));
+  j.there = true;
+  j.col = column * BN;
+  j.row = uniform(int(row));
+  j.m_end = uniform(int(m_end));
+  j.k_lo = uniform(int(k_lo));
+  j.k_hi = uniform(int(k_hi));
   if (gridDim.y > 1) {  // this workgroup's share of the summed dimension, in whole steps
-    const int steps = int((k_hi - k_lo + kStep - 1) / kStep);
-    const int64_t lo = k_lo + int64_t(steps) * blockIdx.y / gridDim.y * kStep;
-    k_hi = min(k_hi, k_lo + int64_t(steps) * (blockIdx.y + 1) / gridDim.y * kStep);
-    k_lo = lo;
+    const int steps = uniform((j.k_hi - j.k_lo + Step - 1) / Step);
+    const int lo = j.k_lo + uniform(int(int64_t(steps) * blockIdx.y / gridDim.y)) * Step;
+    j.k_hi = min(j.k_hi, j.k_lo + uniform(int(int64_t(steps) * (blockIdx.y + 1) / gridDim.y)) * Step);
+    j.k_lo = lo;
   }
+  return j;
+}
 
-  f32x4 acc[FM][FN] = {};
-  const int wm = wave / WN * (BM / WM), wn = wave % WN * (BN / WN);
-  if (k_lo < k_hi) {
-    OperandTile<T, AByK, BM, Threads> ta;
-    OperandTile<T, BByK, BN, Threads> tb;
-    ta.init(A, g.lda, row, m_end, k_lo, k_hi);
-    tb.init(B, g.ldb, col, g.n, k_lo, k_hi);
-    FragmentReader<T, AByK, BM, FM> ra;
-    FragmentReader<T, BByK, BN, FN> rb;
-    ra.init(wm);
-    rb.init(wn);
-    // A step is 2 FM rows of fragments (both halves), multiplied one after another. Reads
-    // run Ahead rows ahead: a buffer's last read is done that many rows before its last
-    // products, and there the step's only barrier stands. Behind it the next buffer is
-    // read and the loads of the step after next may overwrite this one, with a whole step
-    // to arrive; the rows still to be multiplied cover the barrier and the first reads.
-    // Loads behind the end give zeros and nothing multiplies them, so no step branches.
-    typedef decltype(ra.read(a0, 0, 0)) vec;
-    constexpr int Rows = 2 * FM, Ahead = FM < 4 ? FM : 4, Ring = 2 * Ahead;
-    static_assert(Rows % Ring == 0, "a ring of fragments");
-    vec fa[Ring], fb[2][FN];
-    auto read_a = [&](const T* la, int r) { fa[r % Ring] = ra.read(la, r % FM, r / FM % 2); };
-    auto read_b = [&](const T* lb, int h) {
-#pragma unroll
-      for (int j = 0; j < FN; ++j) fb[h][j] = rb.read(lb, j, h);
-    };
-    auto products = [&](int r) {
-#pragma unroll
-      for (int j = 0; j < FN; ++j) acc[r % FM][j] = multiply(fb[r / FM][j], fa[r % Ring], acc[r % FM][j]);
-    };
-    int64_t left = k_hi - k_lo;  // of the step being multiplied
+// BM x BN values per tile, WM x WN waves, each (BM / WM) x (BN / WN) by matrix instructions
+// of 16 x 16. Two LDS buffers, one barrier per step. A workgroup computes tile after tile:
+// the loads of a tile's first two steps start before the results of the tile before it are
+// written, so they arrive while bias, activation and stores run.
+template <typename T, bool AByK, bool BByK, int BM, int BN, int WM, int WN>
+__device__ inline void product_tiles(const ProductArgs& g, ProductMode mode, int tiles_m, int tiles_n, unsigned all) {
+  constexpr int Threads = WM * WN * 64, FM = BM / WM / 16, FN = BN / WN / 16;
+  constexpr int kStep = 128 / int(sizeof(T));  // also the values per row of a stored tile
+  constexpr int WTN = BN / WN;                 // columns of a wave
+  __shared__ __attribute__((aligned(1024))) T a0[BM * kStep];
+  __shared__ __attribute__((aligned(1024))) T b0[BN * kStep];
+  __shared__ __attribute__((aligned(1024))) T a1[BM * kStep];
+  __shared__ __attribute__((aligned(1024))) T b1[BN * kStep];
+  __shared__ __attribute__((aligned(1024))) float stages[WM * WN * 16 * WTN];
+  const int tid = threadIdx.x;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / WN * (BM / WM), wn = wave % WN * WTN;
+  // groups leave some of the tiles unused: only those that exist are spread over the XCDs
+  const unsigned tiles = mode == kRaggedM ? unsigned(count_tiles(g.offsets, g.groups, g.m, BM, true)) * tiles_n : all;
+
+  OperandTile<T, AByK, BM, Threads> ta;
+  OperandTile<T, BByK, BN, Threads> tb;
+  FragmentReader<T, AByK, BM, FM> ra;
+  FragmentReader<T, BByK, BN, FN> rb;
+  ra.init(wm);
+  rb.init(wn);
+  auto begin = [&](const TileJob& j) {
+    const int left = j.k_hi - j.k_lo;
+    if (!j.there || left <= 0) return;
+    const T* B = static_cast<const T*>(g.b) + (mode == kRaggedM ? j.group * g.b_stride : 0);
+    ta.init(static_cast<const T*>(g.a), g.lda, j.row, j.m_end, j.k_lo, j.k_hi);
+    tb.init(B, g.ldb, j.col, g.n, j.k_lo, j.k_hi);
     ta.load(a0, left);
     tb.load(b0, left);
     ta.load(a1, left - kStep);
     tb.load(b1, left - kStep);
-    steps_arrived<decltype(ta)::kLoads + decltype(tb)::kLoads>();
-    read_b(b0, 0);
-#pragma unroll
-    for (int r = 0; r < Ahead; ++r) read_a(a0, r);
-    auto step = [&](T* la, T* lb, const T* na, const T* nb) {
-      // the scheduling barriers keep reads from sinking back to their uses
-#pragma unroll
-      for (int r = 0; r < Rows - Ahead; ++r) {
-        if (r == FM - Ahead) read_b(lb, 1);
-        read_a(la, r + Ahead);
-        products(r);
-        __builtin_amdgcn_sched_barrier(0);
-      }
-      steps_arrived<0>();
-      read_b(nb, 0);
-#pragma unroll
-      for (int r = 0; r < Ahead; ++r) {
-        read_a(na, r);
-        products(Rows - Ahead + r);
-        if (r == 0) ta.load(la, left - 2 * kStep);
-        if (r == 1) tb.load(lb, left - 2 * kStep);
-        __builtin_amdgcn_sched_barrier(0);
-      }
-      left -= kStep;
-    };
-    while (true) {
-      step(a0, b0, a1, b1);
-      if (left <= 0) break;
-      step(a1, b1, a0, b0);
-      if (left <= 0) break;
-    }
-    __builtin_amdgcn_s_waitcnt(0x0F70);  // the loads behind the end, before LDS is used again
-    __syncthreads();
-  }
+  };
 
-  // Results go through LDS, a wave's 16 rows at a time and to itself alone, so that
-  // rows are read and written in 16-byte vectors and the epilogue's code exists once.
-  constexpr int WTN = BN / WN, kChunks = WTN / 4;        // 16-byte chunks of fp32 per row
-  constexpr int kLanesPerRow = WTN / 8, kRowsPerPass = 64 / kLanesPerRow;
-  constexpr int kStage = 1;                              // fragments of rows per stage
-  float* const stage = reinterpret_cast<float*>(a0) + wave * (kStage * 16 * WTN);
-  static_assert(kStage * 16 * WTN * 4 * WM * WN <= BM * 128, "the waves' stages fit");
-  const int64_t c = col + wn + (lane % kLanesPerRow) * 8;
-  const int n = int(min(int64_t(8), g.n - c));
-  const Finish<T> finish(g, C, c, n, group, nothing);
+  unsigned id = blockIdx.x;
+  TileJob job = find_job<BM, BN, kStep>(g, mode, id, tiles, tiles_m, tiles_n);
+  begin(job);
+  while (job.there) {
+    f32x4 acc[FM][FN] = {};
+    int left = job.k_hi - job.k_lo;  // of the step being multiplied
+    if (left > 0) {
+      // A step is 2 FM rows of fragments (both halves), multiplied one after another. Reads
+      // run Ahead rows ahead: a buffer's last read is done that many rows before its last
+      // products, and there the step's only barrier stands. Behind it the next buffer is
+      // read and the loads of the step after next may overwrite this one, with a whole step
+      // to arrive; the rows still to be multiplied cover the barrier and the first reads.
+      // Loads behind the end give zeros and nothing multiplies them, so no step branches.
+      typedef decltype(ra.read(a0, 0, 0)) vec;
+      constexpr int Rows = 2 * FM, Ahead = FM < 4 ? FM : 4, Ring = 2 * Ahead;
+      static_assert(Rows % Ring == 0, "a ring of fragments");
+      vec fa[Ring], fb[2][FN];
+      auto read_a = [&](const T* la, int r) { fa[r % Ring] = ra.read(la, r % FM, r / FM % 2); };
+      auto read_b = [&](const T* lb, int h) {
 #pragma unroll
-  for (int i0 = 0; i0 < FM; i0 += kStage) {
+        for (int j = 0; j < FN; ++j) fb[h][j] = rb.read(lb, j, h);
+      };
+      auto products = [&](int r) {
 #pragma unroll
-    for (int i = 0; i < kStage; ++i)
+        for (int j = 0; j < FN; ++j) acc[r % FM][j] = multiply(fb[r / FM][j], fa[r % Ring], acc[r % FM][j]);
+      };
+      steps_arrived();
+      read_b(b0, 0);
+#pragma unroll
+      for (int r = 0; r < Ahead; ++r) read_a(a0, r);
+      auto step = [&](T* la, T* lb, const T* na, const T* nb) {
+        // the scheduling barriers keep reads from sinking back to their uses
+#pragma unroll
+        for (int r = 0; r < Rows - Ahead; ++r) {
+          if (r == FM - Ahead) read_b(lb, 1);
+          read_a(la, r + Ahead);
+          products(r);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        steps_arrived();
+        read_b(nb, 0);
+#pragma unroll
+        for (int r = 0; r < Ahead; ++r) {
+          read_a(na, r);
+          products(Rows - Ahead + r);
+          if (r == 0) ta.load(la, left - 2 * kStep);
+          if (r == 1) tb.load(lb, left - 2 * kStep);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        left -= kStep;
+      };
+      while (true) {
+        step(a0, b0, a1, b1);
+        if (left <= 0) break;
+        step(a1, b1, a0, b0);
+        if (left <= 0) break;
+      }
+      __builtin_amdgcn_s_waitcnt(0x0F70);  // this wave's loads behind the end, before its next ones
+    }
+    id += gridDim.x;
+    const TileJob next = find_job<BM, BN, kStep>(g, mode, id, tiles, tiles_m, tiles_n);
+
+    // Results go through LDS, 16 rows of a wave at a time and to itself alone, so that rows
+    // are read and written in 16-byte vectors.
+    constexpr int kChunks = WTN / 4;  // 16-byte chunks of fp32 per row
+    constexpr int kLanesPerRow = WTN / 8, kRowsPerPass = 64 / kLanesPerRow;
+    const int lane = here(tid & 63);
+    float* const stage = stages + wave * (16 * WTN);
+    const bool nothing = mode == kRaggedM && job.group == g.groups;
+    T* const C = static_cast<T*>(g.c) + (mode == kRaggedK ? job.group * g.c_stride : 0);
+    const int64_t c = job.col + wn + (lane % kLanesPerRow) * 8;
+    const int n = int(min(int64_t(8), g.n - c));
+    const Finish<T> finish(g, C, c, n, job.group, nothing);  // loads the bias: before the next tile's loads
+    // the last reads of this tile's values were before the last barrier, so every wave may
+    // load the next tile's
+    begin(next);
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
 #pragma unroll
       for (int j = 0; j < FN; ++j) {
-        const int r = i * 16 + (lane & 15), chunk = j * 4 + (lane >> 4);
-        *reinterpret_cast<f32x4*>(stage + r * WTN + ((chunk ^ r) % kChunks) * 4) = acc[i0 + i][j];
+        const int r = lane & 15, chunk = j * 4 + (lane >> 4);
+        *reinterpret_cast<f32x4*>(stage + r * WTN + ((chunk ^ r) % kChunks) * 4) = acc[i][j];
       }
-    __builtin_amdgcn_wave_barrier();
+      __builtin_amdgcn_wave_barrier();
 #pragma nounroll
-    for (int r = lane / kLanesPerRow; r < kStage * 16; r += kRowsPerPass) {
-      const int64_t at = row + wm + i0 * 16 + r;
-      if (at >= m_end || n <= 0) continue;
-      const int chunk = (lane % kLanesPerRow) * 2;
-      float v[8];
-      *reinterpret_cast<f32x4*>(v) = *reinterpret_cast<const f32x4*>(stage + r * WTN + ((chunk ^ r) % kChunks) * 4);
-      *reinterpret_cast<f32x4*>(v + 4) =
-          *reinterpret_cast<const f32x4*>(stage + r * WTN + (((chunk + 1) ^ r) % kChunks) * 4);
-      if (g.partial) store8(partial_at(g, blockIdx.y, at, c), true, n, v);
-      else finish.row(at, v);
+      for (int r = lane / kLanesPerRow; r < 16; r += kRowsPerPass) {
+        const int at = job.row + wm + i * 16 + r;
+        if (at >= job.m_end || n <= 0) continue;
+        const int chunk = (lane % kLanesPerRow) * 2;
+        float v[8];
+        *reinterpret_cast<f32x4*>(v) = *reinterpret_cast<const f32x4*>(stage + r * WTN + ((chunk ^ r) % kChunks) * 4);
+        *reinterpret_cast<f32x4*>(v + 4) =
+            *reinterpret_cast<const f32x4*>(stage + r * WTN + (((chunk + 1) ^ r) % kChunks) * 4);
+        if (g.partial) store8(partial_at(g, blockIdx.y, at, c), true, n, v);
+        else finish.row(at, v);
+      }
+      __builtin_amdgcn_wave_barrier();
     }
-    __builtin_amdgcn_wave_barrier();
+    job = next;
   }
 }
 
 // Two waves per SIMD: half of the registers each.
 template <typename T, bool AByK, bool BByK, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(WM* WN * 64, 2) void product_tile_kernel(ProductArgs g, ProductMode mode, int tiles_m,
-                                                                      int tiles_n) {
-  product_tile<T, AByK, BByK, BM, BN, WM, WN>(g, mode, tiles_m, tiles_n);
+                                                                      int tiles_n, unsigned tiles) {
+  product_tiles<T, AByK, BByK, BM, BN, WM, WN>(g, mode, tiles_m, tiles_n, tiles);
 }
 
 template <typename T, int BM, int BN, int WM, int WN>
 int launch_tile(bool a_by_k, bool b_by_k, ProductMode mode, const ProductArgs& g, int splits, hipStream_t s,
                 std::string* err) {
+  constexpr int kUnits = 256, kXcds = 8;
+  constexpr int kResident = 163840 / ((BM + BN) * 256 + WM * BN * 64);  // by LDS
   const int64_t tiles_n = (g.n + BN - 1) / BN, tiles_m = (g.m + BM - 1) / BM;
-  const int64_t grid = mode == kRaggedK ? g.groups * tiles_m * tiles_n
-                       : mode == kRaggedM ? (tiles_m + g.groups) * tiles_n : tiles_m * tiles_n;
-  if (grid > 0x7fffff) {  // a grid holds less than 2^32 threads
-    *err = "product: more than 2^23 tiles";
+  const int64_t tiles = mode == kRaggedK ? g.groups * tiles_m * tiles_n
+                        : mode == kRaggedM ? (tiles_m + g.groups) * tiles_n : tiles_m * tiles_n;
+  if (tiles > 0x7fffffff) {
+    *err = "product: more than 2^31 tiles";
     return CCL_ERR_INVALID_ARGUMENT;
   }
-  if (grid == 0) return CCL_OK;
+  if (tiles == 0) return CCL_OK;
+  // as many workgroups as are resident at a time, a multiple of the XCDs
+  const int64_t grid = std::min<int64_t>(tiles, std::max<int64_t>(kXcds, kUnits * kResident / splits / kXcds * kXcds));
   auto go = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, dim3(unsigned(grid), splits), dim3(WM * WN * 64), 0, s, g, mode, int(tiles_m), int(tiles_n));
+    hipLaunchKernelGGL(kernel, dim3(unsigned(grid), splits), dim3(WM * WN * 64), 0, s, g, mode, int(tiles_m), int(tiles_n),
+                       unsigned(tiles));
   };
   if (a_by_k && b_by_k) go(product_tile_kernel<T, true, true, BM, BN, WM, WN>);
   else if (b_by_k) go(product_tile_kernel<T, false, true, BM, BN, WM, WN>);

@@ -231,7 +231,6 @@ void choose_tile(int dtype, ProductMode mode, const ProductArgs& g, ProductPlan&
     const double bands = mode == kRaggedM && g.groups > 1 ? double(g.m) / z.edge + 0.5 * std::min<int64_t>(g.groups, g.m)
                                                           : double(up(g.m, z.edge));
     const double tiles = std::max(1.0, bands) * double(up(g.n, z.edge)) * (mode == kRaggedK ? g.groups : 1);
-    if (tiles > (1 << 22)) continue;
     for (int splits : {1, 2, 3, 4, 6, 8, 12, 16}) {
       if (splits > 1 && (mode == kRaggedK || steps < 4 * splits)) break;
       const int64_t each = int64_t(std::ceil(tiles * splits / kUnits));  // workgroups per compute unit
