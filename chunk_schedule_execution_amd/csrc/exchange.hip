@@ -166,6 +166,17 @@ struct __attribute__((aligned(sizeof(T) * V))) Pack {
   T v[V];
 };
 
+// A store around the caches, for rows that are written once and whole.
+template <typename T, int V>
+__device__ inline void stream(Pack<T, V>* to, const Pack<T, V>& x) {
+  if constexpr (sizeof(x) == 16) {
+    typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+    __builtin_nontemporal_store(__builtin_bit_cast(u32x4, x), reinterpret_cast<u32x4*>(to));
+  } else {
+    *to = x;
+  }
+}
+
 template <typename T, int V>
 __global__ __launch_bounds__(256) void dispatch_kernel(const T* x, int64_t ldx, const int32_t* slots, int64_t count,
                                                        int choices, int64_t width, T* rows, int64_t ldr) {
@@ -178,7 +189,7 @@ __global__ __launch_bounds__(256) void dispatch_kernel(const T* x, int64_t ldx, 
   P* dst = reinterpret_cast<P*>(rows + i * ldr);
   const int64_t n = width / V;
   const P zero = {};
-  for (int64_t c = threadIdx.x & 63; c < n; c += 64) dst[c] = here ? src[c] : zero;
+  for (int64_t c = threadIdx.x & 63; c < n; c += 64) stream(dst + c, here ? src[c] : zero);
 }
 
 template <typename T, int V>
@@ -202,7 +213,7 @@ __global__ __launch_bounds__(256) void combine_kernel(const T* h, int64_t ldh, c
   P o;
 #pragma unroll
   for (int q = 0; q < V; ++q) o.v[q] = narrow<T>(sum[q]);
-  reinterpret_cast<P*>(out + t * ldo)[c] = o;
+  stream(reinterpret_cast<P*>(out + t * ldo) + c, o);
 }
 
 // One wave per token: dout's row is read once and stays in registers (Held packs per lane;
@@ -276,7 +287,7 @@ __global__ __launch_bounds__(256) void combine_backward_kernel(const T* dout, in
               P o;
 #pragma unroll
               for (int q = 0; q < V; ++q) o.v[q] = narrow<T>(scale * widen(d[i].v[q]));
-              dst[c0 + i * 64 + lane] = o;
+              stream(dst + c0 + i * 64 + lane, o);
             }
         }
       }

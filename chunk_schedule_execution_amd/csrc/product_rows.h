@@ -39,38 +39,37 @@ __device__ inline f32x4 multiply_rows(f32x4 x, f32x4 y, f32x4 acc) {
   return acc;
 }
 
-// A workgroup computes 16 FM rows by 16 FN columns. Its four waves split the summed
+// A workgroup computes 16 rows by 16 FN columns. Its four waves split the summed
 // dimension by lines of 128 bytes, every operand value goes straight from memory into the
 // registers of a matrix instruction (nothing is used twice within a workgroup, so LDS
 // would only add a trip), and Deep lines per wave are in flight together. The waves' sums
 // meet in LDS in the order of the waves. The summed dimension may also be split over
 // gridDim.y workgroups, whose fp32 sums a second kernel adds up.
-template <typename T, int FM, int FN, bool Vec, int Deep>
+template <typename T, int FN, bool Vec, int Deep>
 __device__ inline void product_rows(const ProductArgs& g, int slabs) {
   constexpr int V = 16 / int(sizeof(T)), kLine = 8 * V;  // values per line of 128 bytes
-  __shared__ float sums[4][FM * 16][FN * 16 + 4];
+  __shared__ float sums[4][16][FN * 16 + 4];
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int band = uniform(blockIdx.x / slabs);
   const int64_t col = int64_t(blockIdx.x - band * slabs) * (16 * FN);
-  const RowTile t = find_tile(g.offsets, g.groups, g.m, 16 * FM, band, true);
+  const RowTile t = find_tile(g.offsets, g.groups, g.m, 16, band, true);
   if (t.group < 0) return;
   const bool nothing = g.offsets && t.group == g.groups;
   const T* A = static_cast<const T*>(g.a);
   const T* B = static_cast<const T*>(g.b) + (nothing ? 0 : t.group * g.b_stride);
-  f32x4 acc[FM][FN] = {};
+  f32x4 acc[FN] = {};
   if (!nothing) {
     const int k_end = int(g.k), lines = (k_end + kLine - 1) / kLine;
     const int first = int(int64_t(lines) * blockIdx.y / gridDim.y), last = int(int64_t(lines) * (blockIdx.y + 1) / gridDim.y);
-    const T* rows[FM];  // rows behind the end repeat the last one: their results are not stored
+    // rows behind the end repeat the last one: their results are not stored
+    const T* row = A + min(t.row + (lane & 15), t.end - 1) * g.lda;
     const T* cols[FN];
-#pragma unroll
-    for (int i = 0; i < FM; ++i) rows[i] = A + min(t.row + i * 16 + (lane & 15), t.end - 1) * g.lda;
 #pragma unroll
     for (int j = 0; j < FN; ++j) cols[j] = B + min(col + j * 16 + (lane & 15), g.n - 1) * g.ldb;
     const int part = (lane >> 4) * V;
     typedef decltype(load_k<T, Vec>(A, 0, 0)) vec;
     for (int l0 = first + wave; l0 < last; l0 += 4 * Deep) {
-      vec a[Deep][2][FM], b[Deep][2][FN];
+      vec a[Deep][2], b[Deep][2][FN];
 #pragma unroll
       for (int d = 0; d < Deep; ++d) {
         const int k = (l0 + 4 * d) * kLine + part, end = l0 + 4 * d < last ? k_end : 0;
@@ -78,8 +77,7 @@ __device__ inline void product_rows(const ProductArgs& g, int slabs) {
         for (int h = 0; h < 2; ++h) {
 #pragma unroll
           for (int j = 0; j < FN; ++j) b[d][h][j] = load_k<T, Vec>(cols[j], k + h * 4 * V, end);
-#pragma unroll
-          for (int i = 0; i < FM; ++i) a[d][h][i] = load_k<T, Vec>(rows[i], k + h * 4 * V, end);
+          a[d][h] = load_k<T, Vec>(row, k + h * 4 * V, end);
         }
       }
       __builtin_amdgcn_sched_barrier(0);  // loads stay ahead of all products
@@ -88,18 +86,14 @@ __device__ inline void product_rows(const ProductArgs& g, int slabs) {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int i = 0; i < FM; ++i)
-#pragma unroll
-            for (int j = 0; j < FN; ++j) acc[i][j] = multiply_rows(b[d][h][j], a[d][h][i], acc[i][j]);
+          for (int j = 0; j < FN; ++j) acc[j] = multiply_rows(b[d][h][j], a[d][h], acc[j]);
     }
 #pragma unroll
-    for (int i = 0; i < FM; ++i)
-#pragma unroll
-      for (int j = 0; j < FN; ++j)
-        *reinterpret_cast<f32x4*>(&sums[wave][i * 16 + (lane & 15)][j * 16 + (lane >> 4) * 4]) = acc[i][j];
+    for (int j = 0; j < FN; ++j)
+      *reinterpret_cast<f32x4*>(&sums[wave][lane & 15][j * 16 + (lane >> 4) * 4]) = acc[j];
     __syncthreads();
   }
-  for (int e = threadIdx.x; e < FM * FN * 256; e += 256) {
+  for (int e = threadIdx.x; e < FN * 256; e += 256) {
     const int r = e / (FN * 16), c = e % (FN * 16);
     const int64_t at = t.row + r, n = col + c;
     if (at >= t.end || n >= g.n) continue;
@@ -109,9 +103,9 @@ __device__ inline void product_rows(const ProductArgs& g, int slabs) {
   }
 }
 
-template <typename T, int FM, int FN, bool Vec, int Deep>
+template <typename T, int FN, bool Vec, int Deep>
 __global__ __launch_bounds__(256) void product_rows_kernel(ProductArgs g, int slabs) {
-  product_rows<T, FM, FN, Vec, Deep>(g, slabs);
+  product_rows<T, FN, Vec, Deep>(g, slabs);
 }
 
 }  // namespace

@@ -5,18 +5,18 @@ namespace ccl {
 namespace prod {
 namespace {
 
-template <typename T, int FM, int FN, int Deep>
+template <typename T, int FN, int Deep>
 int go(const ProductArgs& g, const ProductPlan& plan, hipStream_t s, std::string* err) {
-  const int64_t slabs = (g.n + 16 * FN - 1) / (16 * FN), bands = (g.m + 16 * FM - 1) / (16 * FM) + (g.offsets ? g.groups : 0);
+  const int64_t slabs = (g.n + 16 * FN - 1) / (16 * FN), bands = (g.m + 15) / 16 + (g.offsets ? g.groups : 0);
   if (bands * slabs > 0x7fffffff) {
     *err = "product: more than 2^31 workgroups";
     return CCL_ERR_INVALID_ARGUMENT;
   }
   const dim3 grid(unsigned(bands * slabs), plan.splits);
   if (plan.vec)
-    hipLaunchKernelGGL((product_rows_kernel<T, FM, FN, true, Deep>), grid, dim3(256), 0, s, g, int(slabs));
+    hipLaunchKernelGGL((product_rows_kernel<T, FN, true, Deep>), grid, dim3(256), 0, s, g, int(slabs));
   else
-    hipLaunchKernelGGL((product_rows_kernel<T, FM, FN, false, Deep>), grid, dim3(256), 0, s, g, int(slabs));
+    hipLaunchKernelGGL((product_rows_kernel<T, FN, false, Deep>), grid, dim3(256), 0, s, g, int(slabs));
   const hipError_t e = hipGetLastError();
   if (e == hipSuccess) return CCL_OK;
   *err = std::string("product launch: ") + hipGetErrorString(e);
@@ -25,11 +25,7 @@ int go(const ProductArgs& g, const ProductPlan& plan, hipStream_t s, std::string
 
 template <typename T>
 int pick(const ProductArgs& g, const ProductPlan& plan, hipStream_t s, std::string* err) {
-  switch (plan.kind) {
-    case kRows16: return plan.columns == 1 ? go<T, 1, 1, 4>(g, plan, s, err) : go<T, 1, 2, 4>(g, plan, s, err);
-    case kRows32: return plan.columns == 1 ? go<T, 2, 1, 4>(g, plan, s, err) : go<T, 2, 2, 3>(g, plan, s, err);
-    default: return plan.columns == 1 ? go<T, 4, 1, 2>(g, plan, s, err) : go<T, 4, 2, 2>(g, plan, s, err);
-  }
+  return plan.columns == 1 ? go<T, 1, 4>(g, plan, s, err) : go<T, 2, 4>(g, plan, s, err);
 }
 
 }  // namespace

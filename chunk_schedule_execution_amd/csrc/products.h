@@ -39,12 +39,12 @@ __host__ __device__
 inline int64_t partial_ld(int64_t n) { return (n + 3) / 4 * 4; }
 
 // How a product is run, from its sizes alone.
-enum ProductKind : int { kRows16, kRows32, kRows64, kTile64, kTile128, kTile256 };
+enum ProductKind : int { kRows16, kTile64, kTile128, kTile256 };
 struct ProductPlan {
   ProductKind kind = kTile128;
-  int columns = 1;                   // few-row kinds: 16-column fragments per workgroup
+  int columns = 1;                   // kRows16: 16-column fragments per workgroup
   int splits = 1;                    // of the summed dimension
-  bool vec = true;                   // few-row kinds: both operands lie on the 16-byte grid
+  bool vec = true;                   // kRows16: both operands lie on the 16-byte grid
   bool copy_a = false, copy_b = false;  // tiles: operands that are first copied onto that grid
   int64_t ld_a = 0, ld_b = 0;        // of the copies
   int64_t at_a = 0, at_b = 0, at_partial = 0, bytes = 0;  // workspace layout

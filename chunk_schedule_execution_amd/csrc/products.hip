@@ -257,16 +257,18 @@ ProductPlan plan_product(int dtype, bool a_by_k, bool b_by_k, ProductMode mode, 
   const bool on_a = a_grid == kPadded || (a_grid == kByStrides && g.lda % v == 0 && (a_by_k ? g.m : g.k) % v == 0);
   const bool on_b = b_grid == kPadded || (b_grid == kByStrides && g.ldb % v == 0 && (b_by_k ? g.n : g.k) % v == 0);
   auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
-  // Few rows (on average, in the groups): reading the weights bounds the product, and a
-  // tile of 128 rows would leave most of its products unused.
+  // Few rows (16, or on average 8 in a group) are bound by reading the weights, and there
+  // the kernel without LDS has less to wait for: 64 rows over 64 groups of 2048 x 1024 bf16
+  // take 37 us and 45 in tiles of 64, 512 rows 57 and 65, 1 x 4096 x 16384 fp32 64 and 80, 4 x
+  // 1024 x 1024 bf16 4.5 and 9. One large bf16 matrix the tiles read faster (1 x 4096 x 16384:
+  // 32 us and 35). Weights off the 16-byte grid this kernel reads as they are, uncopied.
   const int64_t mean = g.m / g.groups;
-  if (!a_by_k && !b_by_k && mode != kRaggedK && mean <= 48 && g.m <= 64 * int64_t(g.groups) &&
-      up(g.m, 16) * up(g.n, 16) < (1 << 23)) {
-    if (g.groups == 1) p.kind = g.m <= 16 ? kRows16 : g.m <= 32 ? kRows32 : kRows64;
-    else p.kind = mean <= 8 ? kRows16 : mean <= 20 ? kRows32 : kRows64;
+  const bool few = g.groups > 1 ? mean <= 8 : g.m <= 16;
+  if (!a_by_k && !b_by_k && mode != kRaggedK && few && up(g.m, 16) * up(g.n, 16) < (1 << 23) &&
+      (dtype == CCL_F32 || g.groups > 1 || !on_a || !on_b || g.n * g.k * size <= (32 << 20))) {
+    p.kind = kRows16;
     p.vec = on_a && on_b;
-    const int64_t height = p.kind == kRows16 ? 16 : p.kind == kRows32 ? 32 : 64;
-    const int64_t bands = up(g.m, height) + (g.groups > 1 ? std::min<int64_t>(g.groups, g.m) : 0);
+    const int64_t bands = up(g.m, 16) + (g.groups > 1 ? std::min<int64_t>(g.groups, g.m) : 0);
     p.columns = bands * up(g.n, 32) >= 512 ? 2 : 1;
     const int64_t wgs = std::max<int64_t>(1, bands * up(g.n, 16 * p.columns));
     p.splits = int(std::max<int64_t>(1, std::min<int64_t>(512 / wgs, g.k * size / 4096)));
@@ -307,7 +309,7 @@ int launch_product(int dtype, bool a_by_k, bool b_by_k, ProductMode mode, const 
   }
   if (plan.splits > 1) g.partial = reinterpret_cast<float*>(ws + plan.at_partial);
   int rc;
-  if (plan.kind <= kRows64) rc = launch_rows(dtype, g, plan, s, err);
+  if (plan.kind == kRows16) rc = launch_rows(dtype, g, plan, s, err);
   else if (dtype == CCL_BF16) rc = launch_tile_bf16(a_by_k, b_by_k, mode, g, plan, s, err);
   else rc = launch_tile_f32(a_by_k, b_by_k, mode, g, plan, s, err);
   if (rc || plan.splits == 1) return rc;
