@@ -45,28 +45,28 @@ struct OperandTile {
   int voff[kLoads];
   int kc;  // by rows: first k value of this lane's chunk
 
+  // What does not depend on the tile.
+  __device__ inline void init(int64_t ld) {
+    const int tid = threadIdx.x;
+    ld_bytes = unsigned(ld * kSize);
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int q = i * Threads + tid, r = q / kChunks;  // stored row
+      const int c = (q % kChunks) ^ (ByK ? swizzle(r) : r & 7);
+      voff[i] = int(unsigned(r) * ld_bytes) + c * 16;
+      kc = c * kVec;  // by rows the same for every i: rows differ by multiples of 8
+    }
+  }
+
   // row: first row (or column) of the tile, end: one past the last; k_lo, k_hi: the summed
   // range. The vector around the last value is read whole.
-  __device__ inline void init(const T* p, int64_t ld, int64_t row, int64_t end, int64_t k_lo, int64_t k_hi) {
-    const int tid = here(threadIdx.x);
-    ld_bytes = unsigned(ld * kSize);
+  __device__ inline void place(const T* p, int row, int end, int k_lo, int k_hi) {
     if constexpr (ByK) {
-      base = reinterpret_cast<const char*>(p + k_lo * ld + row);
-      records = unsigned(min(int64_t(R), end - row) + kVec - 1) / kVec * 16;  // whole vectors
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i) {
-        const int q = i * Threads + tid, k = q / kChunks, c = (q % kChunks) ^ swizzle(k);
-        voff[i] = int(unsigned(k) * ld_bytes) + c * 16;
-      }
+      base = reinterpret_cast<const char*>(p + row) + int64_t(k_lo) * ld_bytes;
+      records = unsigned(min(R, end - row) + kVec - 1) / kVec * 16;  // whole vectors
     } else {
-      base = reinterpret_cast<const char*>(p + row * ld + k_lo);
-      records = unsigned(min(int64_t(R), end - row) - 1) * ld_bytes + unsigned(k_hi - k_lo + kVec - 1) / kVec * 16;
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i) {
-        const int q = i * Threads + tid, r = q / 8, c = (q % 8) ^ (r & 7);
-        voff[i] = int(unsigned(r) * ld_bytes) + c * 16;
-        kc = c * kVec;  // the same for every i: rows differ by multiples of 8
-      }
+      base = reinterpret_cast<const char*>(p + k_lo) + int64_t(row) * ld_bytes;
+      records = unsigned(min(R, end - row) - 1) * ld_bytes + unsigned(k_hi - k_lo + kVec - 1) / kVec * 16;
     }
     base = uniform(base);
     records = uniform(int(records));
@@ -245,14 +245,16 @@ __device__ inline void product_tiles(const ProductArgs& g, ProductMode mode, int
   OperandTile<T, BByK, BN, Threads> tb;
   FragmentReader<T, AByK, BM, FM> ra;
   FragmentReader<T, BByK, BN, FN> rb;
+  ta.init(g.lda);
+  tb.init(g.ldb);
   ra.init(wm);
   rb.init(wn);
   auto begin = [&](const TileJob& j) {
     const int left = j.k_hi - j.k_lo;
     if (!j.there || left <= 0) return;
     const T* B = static_cast<const T*>(g.b) + (mode == kRaggedM ? j.group * g.b_stride : 0);
-    ta.init(static_cast<const T*>(g.a), g.lda, j.row, j.m_end, j.k_lo, j.k_hi);
-    tb.init(B, g.ldb, j.col, g.n, j.k_lo, j.k_hi);
+    ta.place(static_cast<const T*>(g.a), j.row, j.m_end, j.k_lo, j.k_hi);
+    tb.place(B, j.col, int(g.n), j.k_lo, j.k_hi);
     ta.load(a0, left);
     tb.load(b0, left);
     ta.load(a1, left - kStep);
@@ -331,7 +333,8 @@ __device__ inline void product_tiles(const ProductArgs& g, ProductMode mode, int
     T* const C = static_cast<T*>(g.c) + (mode == kRaggedK ? job.group * g.c_stride : 0);
     const int64_t c = job.col + wn + (lane % kLanesPerRow) * 8;
     const int n = int(min(int64_t(8), g.n - c));
-    const Finish<T> finish(g, C, c, n, job.group, nothing);  // loads the bias: before the next tile's loads
+    // loads the bias: before the next tile's loads
+    Finish<T> finish(g, C, job.row + wm + lane / kLanesPerRow, kRowsPerPass, c, n, job.group, nothing);
     // the last reads of this tile's values were before the last barrier, so every wave may
     // load the next tile's
     begin(next);
@@ -344,7 +347,7 @@ __device__ inline void product_tiles(const ProductArgs& g, ProductMode mode, int
       }
       __builtin_amdgcn_wave_barrier();
 #pragma nounroll
-      for (int r = lane / kLanesPerRow; r < 16; r += kRowsPerPass) {
+      for (int r = lane / kLanesPerRow; r < 16; r += kRowsPerPass, finish.next()) {
         const int at = job.row + wm + i * 16 + r;
         if (at >= job.m_end || n <= 0) continue;
         const int chunk = (lane % kLanesPerRow) * 2;
@@ -353,7 +356,7 @@ __device__ inline void product_tiles(const ProductArgs& g, ProductMode mode, int
         *reinterpret_cast<f32x4*>(v + 4) =
             *reinterpret_cast<const f32x4*>(stage + r * WTN + (((chunk + 1) ^ r) % kChunks) * 4);
         if (g.partial) store8(partial_at(g, blockIdx.y, at, c), true, n, v);
-        else finish.row(at, v);
+        else finish.row(v);
       }
       __builtin_amdgcn_wave_barrier();
     }

@@ -65,9 +65,9 @@ __global__ __launch_bounds__(256) void join_kernel(ProductArgs g, int splits) {
   const bool nothing = g.offsets && t.group == g.groups;
   const int64_t end = min(t.end, t.row + kJoinRows);
   const int n = int(min(int64_t(8), g.n - c));
-  const Finish<T> finish(g, static_cast<T*>(g.c), c, n, t.group, nothing);
-#pragma unroll 2
-  for (int64_t r = t.row + (threadIdx.x >> 5); r < end; r += 8) {
+  const int64_t first = t.row + (threadIdx.x >> 5);
+  Finish<T> finish(g, static_cast<T*>(g.c), first, 8, c, n, t.group, nothing);
+  for (int64_t r = first; r < end; r += 8) {
     float z[8] = {};
     if (!nothing) {
 #pragma unroll 4
@@ -78,7 +78,8 @@ __global__ __launch_bounds__(256) void join_kernel(ProductArgs g, int splits) {
         for (int q = 0; q < 8; ++q) z[q] += v[q];
       }
     }
-    finish.row(r, z);
+    finish.row(z);
+    finish.next();
   }
 }
 

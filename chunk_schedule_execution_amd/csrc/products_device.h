@@ -305,41 +305,51 @@ __device__ inline bool on_vectors(const void* p, int64_t ld) {
   return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * sizeof(T) % 16 == 0;
 }
 
-// Bias, activation, residual and stores of results, 8 columns (c .. c + n - 1, n <= 8) of a
-// row at a time.
+// Bias, activation, residual and stores of results: 8 columns (c .. c + n - 1, n <= 8) of
+// rows that lie a fixed step apart.
 template <typename T>
 struct Finish {
   const T* residual;
   T* preact;
   T* out;
-  int64_t ldr, ldp, ldc, c;
+  int64_t step_r, step_p, step_c;  // elements from one of its rows to the next
   float bias[8];
   int n, act;
-  bool vec_c, vec_r, vec_p, nothing;
+  bool vec_c, vec_r, vec_p, with_bias;
 
   // nothing: rows of no group, whose results are zeros (z has to be 0)
-  __device__ inline Finish(const ProductArgs& g, T* to, int64_t column, int count, int group, bool none)
-      : residual(static_cast<const T*>(g.residual)), preact(static_cast<T*>(g.preact)), out(to), ldr(g.ldr),
-        ldp(g.ldp), ldc(g.ldc), c(column), n(count), act(none ? CCL_ACT_NONE : g.act), nothing(none) {
-    vec_c = on_vectors<T>(out, ldc);
-    vec_r = on_vectors<T>(residual, ldr);
-    vec_p = on_vectors<T>(preact, ldp);
-#pragma unroll
-    for (int q = 0; q < 8; ++q) bias[q] = 0.0f;
-    if (g.bias && !none && n > 0) load8(static_cast<const T*>(g.bias) + group * g.bias_stride + c, false, n, bias);
+  __device__ inline Finish(const ProductArgs& g, T* to, int64_t row, int step, int64_t c, int count, int group,
+                           bool nothing)
+      : residual(static_cast<const T*>(g.residual)), preact(static_cast<T*>(g.preact)), out(to + row * g.ldc + c),
+        step_r(step * g.ldr), step_p(step * g.ldp), step_c(step * g.ldc), n(count),
+        act(nothing ? CCL_ACT_NONE : g.act) {
+    vec_c = on_vectors<T>(to, g.ldc);
+    vec_r = on_vectors<T>(residual, g.ldr);
+    vec_p = on_vectors<T>(preact, g.ldp);
+    if (residual) residual += row * g.ldr + c;
+    if (preact) preact += row * g.ldp + c;
+    with_bias = g.bias != nullptr && !nothing;
+    if (with_bias && n > 0) load8(static_cast<const T*>(g.bias) + group * g.bias_stride + c, false, n, bias);
   }
-  __device__ inline void row(int64_t r, float* z) const {
+  __device__ inline void row(float* z) const {
+    if (with_bias) {
 #pragma unroll
-    for (int q = 0; q < 8; ++q) z[q] += bias[q];
-    if (preact) store8<true>(preact + r * ldp + c, vec_p, n, z);
+      for (int q = 0; q < 8; ++q) z[q] += bias[q];
+    }
+    if (preact) store8<true>(preact, vec_p, n, z);
     act8(z, act);
     if (residual) {
       float w[8];
-      load8(residual + r * ldr + c, vec_r, n, w);
+      load8(residual, vec_r, n, w);
 #pragma unroll
       for (int q = 0; q < 8; ++q) z[q] += w[q];
     }
-    store8<true>(out + r * ldc + c, vec_c, n, z);
+    store8<true>(out, vec_c, n, z);
+  }
+  __device__ inline void next() {
+    out += step_c;
+    if (preact) preact += step_p;
+    if (residual) residual += step_r;
   }
 };
 
