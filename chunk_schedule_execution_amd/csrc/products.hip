@@ -25,30 +25,33 @@ int hip_status(const char* what, std::string* err) {
 }
 
 // ---- operands off the 16-byte grid ------------------------------------------------------
-// Rows copied to a stride of whole vectors, zeros behind their end. One pass over the
-// operand, so it costs what reading and writing it costs; reading such rows element by
-// element in the tiles costs more from a few tiles per row on.
+// Rows copied to a stride of whole vectors, zeros behind their end: one pass over the
+// operand, 5 us for the 1111 x 1001 of an odd product. Both operands in one launch.
+struct Regrid {
+  const void* src = nullptr;
+  void* dst = nullptr;
+  int64_t ld = 0, rows = 0, len = 0, ld_dst = 0;
+};
+
 template <typename T>
-__global__ __launch_bounds__(256) void regrid_kernel(const T* src, int64_t ld, int64_t rows, int64_t len, T* dst,
-                                                     int64_t ld_dst) {
+__global__ __launch_bounds__(256) void regrid_kernel(Regrid first, Regrid second) {
+  const Regrid g = blockIdx.z ? second : first;
+  const T* src = static_cast<const T*>(g.src);
+  T* dst = static_cast<T*>(g.dst);
   const int64_t c = int64_t(blockIdx.y) * 1024 + threadIdx.x;
-  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x)
+  for (int64_t r = blockIdx.x; r < g.rows; r += gridDim.x)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int64_t at = c + i * 256;
-      if (at < ld_dst) dst[r * ld_dst + at] = at < len ? src[r * ld + at] : T(0.0f);
+      if (at < g.ld_dst) dst[r * g.ld_dst + at] = at < g.len ? src[r * g.ld + at] : T(0.0f);
     }
 }
 
-int regrid(int dtype, const void* src, int64_t ld, int64_t rows, int64_t len, void* dst, int64_t ld_dst, hipStream_t s,
-           std::string* err) {
-  const dim3 grid(unsigned(std::min<int64_t>(rows, 1 << 20)), unsigned((ld_dst + 1023) / 1024));
-  if (dtype == CCL_BF16)
-    hipLaunchKernelGGL(regrid_kernel<bf16>, grid, dim3(256), 0, s, static_cast<const bf16*>(src), ld, rows, len,
-                       static_cast<bf16*>(dst), ld_dst);
-  else
-    hipLaunchKernelGGL(regrid_kernel<float>, grid, dim3(256), 0, s, static_cast<const float*>(src), ld, rows, len,
-                       static_cast<float*>(dst), ld_dst);
+int regrid(int dtype, const Regrid& first, const Regrid& second, hipStream_t s, std::string* err) {
+  const dim3 grid(unsigned(std::min<int64_t>(std::max(first.rows, second.rows), 1 << 20)),
+                  unsigned((std::max(first.ld_dst, second.ld_dst) + 1023) / 1024), second.rows ? 2 : 1);
+  if (dtype == CCL_BF16) hipLaunchKernelGGL(regrid_kernel<bf16>, grid, dim3(256), 0, s, first, second);
+  else hipLaunchKernelGGL(regrid_kernel<float>, grid, dim3(256), 0, s, first, second);
   return hip_status("regrid launch", err);
 }
 
@@ -295,19 +298,24 @@ int launch_product(int dtype, bool a_by_k, bool b_by_k, ProductMode mode, const 
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   ProductArgs g = args;
   unsigned char* ws = static_cast<unsigned char*>(workspace);
+  Regrid copy[2];
+  int copies = 0;
   if (plan.copy_a) {
-    if (int rc = regrid(dtype, g.a, g.lda, a_by_k ? g.k : g.m, a_by_k ? g.m : g.k, ws + plan.at_a, plan.ld_a, s, err)) return rc;
+    copy[copies++] = {g.a, ws + plan.at_a, g.lda, a_by_k ? g.k : g.m, a_by_k ? g.m : g.k, plan.ld_a};
     g.a = ws + plan.at_a;
     g.lda = plan.ld_a;
   }
   if (plan.copy_b) {
     // the groups' matrices follow each other, so their rows are one run of rows
     const int64_t rows = (b_by_k ? g.k : g.n) * (mode == kRaggedM ? g.groups : 1);
-    if (int rc = regrid(dtype, g.b, g.ldb, rows, b_by_k ? g.n : g.k, ws + plan.at_b, plan.ld_b, s, err)) return rc;
+    copy[copies++] = {g.b, ws + plan.at_b, g.ldb, rows, b_by_k ? g.n : g.k, plan.ld_b};
     g.b = ws + plan.at_b;
     g.ldb = plan.ld_b;
     g.b_stride = (b_by_k ? g.k : g.n) * plan.ld_b;
   }
+  // (no rows: the gradient of no rows, whose products are empty sums)
+  if (copies && std::max(copy[0].rows, copy[1].rows) > 0)
+    if (int rc = regrid(dtype, copy[0], copy[1], s, err)) return rc;
   if (plan.splits > 1) g.partial = reinterpret_cast<float*>(ws + plan.at_partial);
   int rc;
   if (plan.kind == kRows16) rc = launch_rows(dtype, g, plan, s, err);

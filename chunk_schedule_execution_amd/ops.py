@@ -89,9 +89,14 @@ def _ld(t, name: str) -> int:
     return ld
 
 
+# the handle alone, without a Stream object around it (0.1 us instead of 1.9)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
 def _stream(stream, device: int) -> int:
     if stream is None:
-        return torch.cuda.current_stream(device).cuda_stream
+        return _raw_stream(device)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
