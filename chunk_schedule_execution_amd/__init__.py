@@ -7,6 +7,9 @@ allocation -- and one HIP kernel launch runs the whole collective over P virtual
 ranks that share the GPU's HBM. ``capi`` is the ctypes binding of ``include/ccl.h``
 under the same names; ``plan.Plan`` is a small object wrapper over it.
 
+``ops`` (imported on its own, it needs torch) holds the products of sharded layers and the
+row exchange around an expert-parallel layer's AllToAlls, over torch tensors.
+
 Importing this package loads ``lib/libccl.so`` and fails if it is not built.
 """
 

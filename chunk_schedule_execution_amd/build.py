@@ -1,7 +1,7 @@
 """Build libccl.so in-tree with hipcc for gfx950.
 
-One shared library holds the host compiler, the plan runtime, the C entry points and
-the executor kernel. Host sources are plain C++17; the kernel source is HIP. Every
+One shared library holds the host compiler, the plan runtime, the C entry points, the
+executor kernel and the kernels of the products and the row exchange. Host sources are plain C++17; the kernel source is HIP. Every
 file is compiled with packed-fp32 instructions disabled.
 """
 

@@ -1,6 +1,8 @@
 // The row exchange around an expert-parallel layer's AllToAlls for gfx950: routing (a
 // stable counting sort of the choices by expert), dispatch, combine and its gradients.
 // All of it is memory traffic; rows move as 16-byte vectors where they lie on that grid.
+// 16384 tokens of 4 choices and 4096 bf16: combine 671 MB in 129 us, 5.2 TB/s; its gradient
+// 1.21 GB in 303 us, 4.0 TB/s (a copy of 1 GB reaches 4.9).
 #include <algorithm>
 
 #include "products_device.h"
@@ -146,7 +148,10 @@ __global__ __launch_bounds__(1024) void route_small_kernel(const int32_t* ids, i
   walk_chunk<true>(ids, lo, hi, experts, bits, count[wave], positions, slot_of);
   for (int i = used + tid; i < slots; i += 1024) slot_of[i] = -1;
 }
-constexpr int64_t kSmallRoute = 8192;  // one kernel 7 us against three kernels' 8 and their launches' 18 at 192 slots
+// One kernel takes 3.2 us at 192 slots, the three of a long route 2.5 to 3 us each and a launch
+// more; a wave of the one kernel walks 8 rounds of 64 slots at this length, as many as a
+// chunk's of the three.
+constexpr int64_t kSmallRoute = 8192;
 
 struct RoutePlan {
   int64_t chunk;
@@ -216,7 +221,8 @@ __global__ __launch_bounds__(256) void combine_kernel(const T* h, int64_t ldh, c
   stream(reinterpret_cast<P*>(out + t * ldo) + c, o);
 }
 
-// One wave per token: dout's row is read once and stays in registers (Held packs per lane;
+// One wave per token: dout's row is read once (a wave per row of h read it once per choice:
+// 313 us in place of 303) and stays in registers (Held packs per lane;
 // longer rows take several rounds), then for each choice h's row is read, its product with
 // dout summed and dh's row written. The blocks behind the tokens' look for rows that no
 // slot has and clear them.

@@ -43,7 +43,9 @@ __device__ inline f32x4 multiply_rows(f32x4 x, f32x4 y, f32x4 acc) {
 // dimension by lines of 128 bytes, every operand value goes straight from memory into the
 // registers of a matrix instruction (nothing is used twice within a workgroup, so LDS
 // would only add a trip), and Deep lines per wave are in flight together. The waves' sums
-// meet in LDS in the order of the waves. The summed dimension may also be split over
+// meet in LDS in the order of the waves. Bound by reading the weights: the 41 used of 64
+// matrices of 2048 x 1024 bf16 in 26 us warm and 33 cold, 5.2 TB/s. Two sets of registers in
+// flight instead of more waves lost (1 x 4096 x 16384: 41 us and 35). The summed dimension may also be split over
 // gridDim.y workgroups, whose fp32 sums a second kernel adds up.
 template <typename T, int FN, bool Vec, int Deep>
 __device__ inline void product_rows(const ProductArgs& g, int slabs) {
