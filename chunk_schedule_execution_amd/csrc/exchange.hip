@@ -222,10 +222,10 @@ __global__ __launch_bounds__(256) void combine_kernel(const T* h, int64_t ldh, c
 }
 
 // One wave per token: dout's row is read once (a wave per row of h read it once per choice:
-// 313 us in place of 303) and stays in registers (Held packs per lane;
-// longer rows take several rounds), then for each choice h's row is read, its product with
-// dout summed and dh's row written. The blocks behind the tokens' look for rows that no
-// slot has and clear them.
+// 313 us in place of 303) and stays in registers (Held packs per lane; longer rows take
+// several rounds), then for each choice h's row is read, its product with dout summed and
+// dh's row written. The blocks behind the tokens' look for rows that no slot has and clear
+// them.
 template <typename T, int V, int Held>
 __global__ __launch_bounds__(256) void combine_backward_kernel(const T* dout, int64_t ldo, const T* h, int64_t ldh,
                                                                const int32_t* positions, const int32_t* slots,

@@ -214,7 +214,10 @@ namespace {
 // less per product but leaves units idle: 2048^2 x 4096 takes 47 us in 64s or 128s and
 // 87 in 256s, 4096^2 x 4096 189, 130 and 112. Splits cost a second kernel (5 us) and the
 // partial sums' way through memory (written and read at 3.5 TB/s): 512^2 x 4096 takes 31 us
-// unsplit and 17 in 4 splits of 64s, 1024^2 x 1024 11 and 16 in 2.
+// unsplit and 17 in 4 splits of 64s, 1024^2 x 1024 11 and 16 in 2. Operands from memory are
+// read at 5.6 TB/s at best, and slower by few workgroups, whose two steps in flight are too
+// little: 32 x 4096 x 16384 in 64s takes 54 us unsplit (one workgroup per unit), 42 in 2
+// splits and 36 in 4.
 void choose_tile(int dtype, ProductMode mode, const ProductArgs& g, ProductPlan& p) {
   struct Size {
     ProductKind kind;
@@ -229,6 +232,8 @@ void choose_tile(int dtype, ProductMode mode, const ProductArgs& g, ProductPlan&
   constexpr int64_t kUnits = 256;
   const double summed = double(mode == kRaggedK ? g.k / std::max(1, g.groups) : g.k);
   const double steps = std::max(1.0, std::ceil(summed * (dtype == CCL_BF16 ? 2 : 4) / 128));
+  const double weights = double(g.n) * double(g.k) * (mode == kRaggedM ? g.groups : 1);
+  const double bytes = (double(g.m) * double(g.k) + weights) * (dtype == CCL_BF16 ? 2 : 4);
   double best = 0;
   for (int i = 0; i < count; ++i) {
     const Size& z = sizes[i];
@@ -241,7 +246,9 @@ void choose_tile(int dtype, ProductMode mode, const ProductArgs& g, ProductPlan&
       const int64_t each = int64_t(std::ceil(tiles * splits / kUnits));  // workgroups per compute unit
       auto step = [&](int64_t n) { return z.resident == 1 || n <= 1 ? z.alone * n : z.alone + (z.full - z.alone) * (n - 1) / (z.resident - 1); };
       const double rounds = double(each / z.resident);
-      double us = std::ceil(steps / splits) * (rounds * step(z.resident) + step(each % z.resident)) + z.ends * (rounds + (each % z.resident != 0));
+      double us = std::ceil(steps / splits) * (rounds * step(z.resident) + step(each % z.resident));
+      const double rate = std::min(5.6, 1.4 + 1.4 * z.edge / 64 * double(std::min<int64_t>(each, z.resident)));  // MB per us
+      us = std::max(us, bytes / (rate * 1e6)) + z.ends * (rounds + (each % z.resident != 0));
       if (splits > 1) us += 5 + 2.0 * splits * double(g.m) * double(g.n) * 4 / 3.5e6;
       if (best == 0 || us < best) {
         best = us;

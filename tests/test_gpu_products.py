@@ -258,6 +258,33 @@ def test_grouped_nan_stays_in_its_group():
     assert torch.equal(dw[0], clean[1][0]) and torch.equal(dw[2], clean[1][2])
 
 
+# ---- the largest tiles, several of them per workgroup ---------------------------------------
+@pytest.mark.parametrize("rows,k,n,act,residual,save,pad", [
+    (4000, 1000, 4088, "gelu", True, True, 8), (8100, 1000, 4088, "none", False, False, 0),
+    (4001, 1001, 4085, "silu", True, True, 3)])
+def test_linear_of_many_large_tiles(rows, k, n, act, residual, save, pad):
+    linear_case(rows, k, n, "bf16", act, bias=True, residual=residual, save=save, pad=pad)
+
+
+@pytest.mark.parametrize("pad", [0, 5])
+def test_linear_backward_of_many_large_tiles(pad):
+    backward_case(4000, 4088, 4096, "bf16", "gelu", pad)
+
+
+def test_grouped_linear_of_many_large_tiles():
+    offsets = [0, 1, 2700, 2700, 6111, 7950]  # the last 50 rows belong to no group
+    grouped_case(8000, 2000, 4088, offsets, "bf16", "gelu_tanh")
+    backward_case(8000, 2000, 4088, "bf16", "silu", offsets=offsets, experts=5)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,k,n", [(40, 16384, 300), (130, 8200, 130), (500, 4104, 72), (33, 16400, 1)])
+def test_linear_of_split_sums(rows, k, n, dtype):
+    linear_case(rows, k, n, dtype, "silu", bias=True, residual=True, save=True)
+    backward_case(n, rows, k, dtype, "gelu")
+    backward_case(k, rows, n, dtype, "none")
+
+
 # ---- as a user has them ---------------------------------------------------------------------
 def test_same_bits_again_and_on_another_stream():
     x, w = normal(1, 700, 520, dtype=torch.bfloat16), normal(2, 264, 520, dtype=torch.bfloat16)
