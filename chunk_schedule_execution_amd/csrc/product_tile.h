@@ -164,19 +164,23 @@ __device__ inline void steps_arrived() {
 }
 
 // Which tile a workgroup computes. Workgroups go round the 8 XCDs, each with an L2 of its
-// own, so XCD x takes the x-th eighth of the tiles; within it 8 bands (rows of tiles) are
-// walked together, column by column, so that the 32 workgroups that run there at a time
-// share 8 row and 4 column tiles: 3 % of 8192^3 (bf16, 760 us) against the order of the columns.
+// own, so XCD x takes the x-th eighth of the tiles; within it kBands bands (rows of tiles)
+// are walked together, column by column, so that the 32 workgroups that run there at a time
+// share, with 8 bands, 8 row and 4 column tiles: 3 % of 8192^3 (bf16, 760 us) against the
+// order of the columns. From each such set to the next the bands turn by one, or a workgroup
+// would meet the same band again and again, and the last bands of groups are shorter than
+// others: 16384 rows over 32 groups, 2048 x 4096, take 340 to 353 us for 346 to 361.
+template <int kBands>
 __device__ inline void place_tile(unsigned id, unsigned tiles, int tiles_n, int& band, int& column) {
   constexpr unsigned kXcds = 8;
-  constexpr int kBands = 8;
   const unsigned x = id % kXcds, whole = tiles / kXcds, rest = tiles % kXcds;
   const int l = int(x * whole + min(x, rest) + id / kXcds);
   // quotients are computed in vector registers: uniform() brings them back
   const int slab = uniform(l / (kBands * tiles_n)), in = l - slab * kBands * tiles_n;
   const int bands = min(kBands, int(tiles) / tiles_n - slab * kBands);
   column = uniform(in / bands);
-  band = slab * kBands + in - column * bands;
+  const int turned = in - column * bands + column / (32 / kBands);
+  band = slab * kBands + turned - uniform(turned / bands) * bands;
 }
 
 // ---- the kernel ---------------------------------------------------------------------------
@@ -193,13 +197,19 @@ __device__ inline TileJob find_job(const ProductArgs& g, ProductMode mode, unsig
   TileJob j;
   if (id >= tiles) return j;
   int band, column;
-  place_tile(id, tiles, tiles_n, band, column);
   int64_t row = 0, m_end = g.m, k_lo = 0, k_hi = g.k;
   if (mode == kRaggedK) {
-    j.group = uniform(band / tiles_m);
-    row = int64_t(band - j.group * tiles_m) * BM;
+    // Group after group, each spread over all XCDs: their lengths differ, and with them the
+    // work. 16 groups of 512 rows +- 30 %, 2048 x 2048, take 104 us; 130 with two whole groups
+    // per XCD, though now every L2 reads the groups' rows. 4 bands by 2 columns of a group's
+    // 64 tiles read less of them than 8 by 1: 3 us.
+    const unsigned per = unsigned(tiles_m) * unsigned(tiles_n);
+    j.group = uniform(int(id / per));
+    place_tile<4>(id - unsigned(j.group) * per, per, tiles_n, band, column);
+    row = int64_t(band) * BM;
     group_bounds(g.offsets, g.k, j.group, k_lo, k_hi);
   } else {
+    place_tile<8>(id, tiles, tiles_n, band, column);
     const RowTile t = find_tile(g.offsets, g.groups, g.m, BM, band, true);
     j.group = uniform(t.group);
     row = t.row;
