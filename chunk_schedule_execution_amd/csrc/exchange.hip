@@ -1,8 +1,8 @@
 // The row exchange around an expert-parallel layer's AllToAlls for gfx950: routing (a
 // stable counting sort of the choices by expert), dispatch, combine and its gradients.
 // All of it is memory traffic; rows move as 16-byte vectors where they lie on that grid.
-// 16384 tokens of 4 choices and 4096 bf16: combine 671 MB in 129 us, 5.2 TB/s; its gradient
-// 1.21 GB in 303 us, 4.0 TB/s (a copy of 1 GB reaches 4.9).
+// 16384 tokens of 4 choices and 4096 bf16: combine 671 MB in 123 us, 5.5 TB/s; its gradient
+// 1.21 GB in 221 us, 5.5 TB/s (a plain copy of 1 GB reaches 4.9).
 #include <algorithm>
 
 #include "products_device.h"
@@ -182,6 +182,18 @@ __device__ inline void stream(Pack<T, V>* to, const Pack<T, V>& x) {
   }
 }
 
+// A load around the caches, of rows that are read once: 6 us of the 129 that combine takes
+// with plain loads, 25 to 60 of its gradient's, with Held as it is.
+template <typename T, int V>
+__device__ inline Pack<T, V> load_once(const Pack<T, V>* from) {
+  if constexpr (sizeof(Pack<T, V>) == 16) {
+    typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+    return __builtin_bit_cast(Pack<T, V>, __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(from)));
+  } else {
+    return *from;
+  }
+}
+
 template <typename T, int V>
 __global__ __launch_bounds__(256) void dispatch_kernel(const T* x, int64_t ldx, const int32_t* slots, int64_t count,
                                                        int choices, int64_t width, T* rows, int64_t ldr) {
@@ -211,7 +223,7 @@ __global__ __launch_bounds__(256) void combine_kernel(const T* h, int64_t ldh, c
     const int p = positions[t * choices + j];
     if (p < 0 || p >= count) continue;
     const float gate = gates ? gates[t * choices + j] : 1.0f;
-    const P v = reinterpret_cast<const P*>(h + p * ldh)[c];
+    const P v = load_once(reinterpret_cast<const P*>(h + p * ldh) + c);
 #pragma unroll
     for (int q = 0; q < V; ++q) sum[q] += gate * widen(v.v[q]);
   }
@@ -221,10 +233,11 @@ __global__ __launch_bounds__(256) void combine_kernel(const T* h, int64_t ldh, c
   stream(reinterpret_cast<P*>(out + t * ldo) + c, o);
 }
 
-// One wave per token: dout's row is read once (a wave per row of h read it once per choice:
-// 313 us in place of 303) and stays in registers (Held packs per lane; longer rows take
-// several rounds), then for each choice h's row is read, its product with dout summed and
-// dh's row written. The blocks behind the tokens' look for rows that no slot has and clear
+// One wave per token: Held packs of dout's row per lane are read once and stay in registers
+// (a wave per row of h read them once per choice: 3 % more), longer rows take several rounds;
+// then for each choice h's row is read, its product with dout summed and dh's row written.
+// Held is 4: 4096 bf16 values of 16384 tokens with 4 choices take 221 us (with 8, fewer waves,
+// 280; with 2, shorter pieces of rows, 284; two rows of h at a time 225). The blocks behind the tokens' look for rows that no slot has and clear
 // them.
 template <typename T, int V, int Held>
 __global__ __launch_bounds__(256) void combine_backward_kernel(const T* dout, int64_t ldo, const T* h, int64_t ldh,
@@ -275,7 +288,7 @@ __global__ __launch_bounds__(256) void combine_backward_kernel(const T* dout, in
           P v[Held];
 #pragma unroll
           for (int i = 0; i < Held; ++i)
-            if (c0 + i * 64 + lane < n) v[i] = hrow[c0 + i * 64 + lane];
+            if (c0 + i * 64 + lane < n) v[i] = load_once(hrow + c0 + i * 64 + lane);
 #pragma unroll
           for (int i = 0; i < Held; ++i)
             if (c0 + i * 64 + lane < n)
@@ -402,8 +415,8 @@ static int combine_backward_t(const void* dout, int64_t ldo, const void* h, int6
   };
   const bool wide = on_grid(dout, ldo, width, sizeof(T)) && (!dgates || on_grid(h, ldh, width, sizeof(T))) &&
                     (!dh || on_grid(dh, lddh, width, sizeof(T)));
-  if (wide) go(combine_backward_kernel<T, V, 8>);
-  else go(combine_backward_kernel<T, 1, 8>);
+  if (wide) go(combine_backward_kernel<T, V, 4>);
+  else go(combine_backward_kernel<T, 1, 4>);
   return hip_status("combine gradient launch", err);
 }
 
