@@ -98,7 +98,8 @@ int join(int dtype, const ProductArgs& g, int splits, hipStream_t s, std::string
 // columns, 8 columns (16 or 32 bytes) per thread, and leaves one fp32 sum per column and
 // tile; a second kernel adds the tiles of a group in order, so the sums do not depend on
 // the order in which workgroups run. Bound by memory: 8192 x 4096 bf16 (two reads, one
-// write, 201 MB) in 42 us, 4.8 TB/s.
+// write, 201 MB) in 42 us, 4.8 TB/s. Both operands are read around the caches, which leaves
+// those to dz for the products behind it: with them 443 us for 449.
 constexpr int kSlopeLanes = 8;  // rows that a workgroup has in hand at a time
 
 // Rows of a tile: 64, fewer where those would not fill the chip, more where a grid could
@@ -125,10 +126,10 @@ __global__ __launch_bounds__(256) void slope_kernel(SlopeArgs g, int height, boo
   for (int64_t r = t.row + lane; r < end; r += kSlopeLanes) {
     float v[8] = {};
     if (!nothing && n > 0) {
-      load8(dout + r * g.ldo + c, vec_o, n, v);
+      load8<true>(dout + r * g.ldo + c, vec_o, n, v);
       if (g.act != CCL_ACT_NONE) {
         float z[8];
-        load8(preact + r * g.ldp + c, vec_p, n, z);
+        load8<true>(preact + r * g.ldp + c, vec_p, n, z);
         slope8(v, z, g.act);
 #pragma unroll
         for (int q = 0; q < 8; ++q) v[q] = q < n ? v[q] : 0.0f;

@@ -230,15 +230,17 @@ __device__ inline void group_tiles(const int32_t* offsets, int groups, int64_t r
 
 // ---- results -----------------------------------------------------------------------------
 // 8 neighbouring values of a row; `vec`: the row lies on the 16-byte grid; `n`: how many of
-// them exist.
-template <typename T>
+// them exist. Stream: around the caches, for what is read once.
+template <bool Stream = false, typename T>
 __device__ inline void load8(const T* p, bool vec, int n, float* v) {
   if (vec && n >= 8) {
     constexpr int V = 16 / int(sizeof(T));
     typedef T pack __attribute__((ext_vector_type(V)));
 #pragma unroll
     for (int h = 0; h < 8 / V; ++h) {
-      const pack x = reinterpret_cast<const pack*>(p)[h];
+      pack x;
+      if constexpr (Stream) x = __builtin_nontemporal_load(reinterpret_cast<const pack*>(p) + h);
+      else x = reinterpret_cast<const pack*>(p)[h];
 #pragma unroll
       for (int q = 0; q < V; ++q) v[h * V + q] = widen(x[q]);
     }
@@ -247,6 +249,7 @@ __device__ inline void load8(const T* p, bool vec, int n, float* v) {
     for (int q = 0; q < 8; ++q) v[q] = q < n ? widen(p[q]) : 0.0f;
   }
 }
+
 // Stream: around the caches, for what is not read again soon. 33 MB of results per round of
 // tiles otherwise push the operands out of the L2s: 16384 rows over 32 experts of 2048 x
 // 4096 take 351 us, and 390 with plain stores.
