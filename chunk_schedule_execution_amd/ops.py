@@ -3,9 +3,13 @@
 Thin wrappers of the ``ccl_linear*``, ``ccl_grouped_linear*`` and ``ccl_expert_*`` entry
 points: they read shapes, strides and types off the tensors, allocate outputs and
 workspace from torch on the call's stream and launch there (torch's current stream of the
-tensors' device unless ``stream`` is given; a call on another stream orders nothing by
-itself, as with ``Plan.execute``). Everything else is in ``libccl.so``. Gradients are
-explicit calls; nothing registers with torch's autograd.
+tensors' device unless ``stream``, a torch stream or a raw handle, is given). A call on
+another stream orders nothing by itself, as with ``Plan.execute``: the caller lets that
+stream wait for the inputs and keeps them (and an ``out`` of its own) until it has passed
+the call. What the call allocates is that stream's, so nothing that torch's current stream
+still works on is written; outputs may be dropped as soon as the current stream's own work
+on them is enqueued. Everything else is in ``libccl.so``. Gradients are explicit calls;
+nothing registers with torch's autograd.
 
 Floating tensors of a call share one type, float32 or bfloat16 (gates are float32).
 Matrices may have rows further apart than their length; their rows must be contiguous.
@@ -94,36 +98,47 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
-def _stream(stream, device: int) -> int:
-    if stream is None:
-        return _raw_stream(device)
-    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-
-
-def _own(stream, *tensors) -> None:
-    """Tells torch's allocator that memory allocated on its current stream is in use on
-    ``stream``, so it is not handed out again before that stream passes the call."""
-    if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
-    for t in tensors:
-        if t is not None and t.numel():
-            t.record_stream(stream)
-
-
 class _on:
-    """The device of a call, made current if it is not."""
+    """The device and the stream of a call, made torch's current ones for its length where
+    they are not, so that memory comes from the pool of the stream that uses it: a block of
+    another stream's pool may still be in use there after its tensor is gone."""
 
-    __slots__ = ("device", "before")
+    __slots__ = ("device", "before", "stream", "handle", "outer", "switch")
 
-    def __init__(self, device: int):
-        self.device = device
+    def __init__(self, device: int, stream):
+        self.device, self.stream, self.switch = device, stream, None
+        if stream is not None:
+            if getattr(stream, "device", None) is not None and stream.device.index != device:
+                _refuse(f"stream: of {stream.device}; one of GPU {device} wanted")
+            self.handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
-    def __enter__(self):
+    def __enter__(self) -> int:
+        """The handle to launch on."""
         self.before = torch.cuda.current_device()
         if self.before != self.device:
             torch.cuda.set_device(self.device)
+        current = _raw_stream(self.device)
+        if self.stream is None:
+            return current
+        if self.handle != current:
+            self.outer = torch.cuda.current_stream()
+            self.switch = torch.cuda.stream(
+                self.stream if isinstance(self.stream, torch.cuda.Stream) else
+                torch.cuda.ExternalStream(self.handle) if self.handle else torch.cuda.default_stream())
+            self.switch.__enter__()
+        return self.handle
+
+    def give(self, *tensors) -> None:
+        """Tells torch's allocator that outputs made here go to the stream that was current:
+        freed, they are not handed out again before it has passed its work on them."""
+        if self.switch is not None:
+            for t in tensors:
+                if t is not None and t.numel():
+                    t.record_stream(self.outer)
 
     def __exit__(self, *a):
+        if self.switch is not None:
+            self.switch.__exit__(*a)
         if self.before != self.device:
             torch.cuda.set_device(self.before)
 
@@ -171,7 +186,8 @@ def _forward(x, w, offsets, bias, residual, activation, save_preact, out, preact
     if residual is not None:
         _like(residual, "residual", (rows, n), dtype, device)
         pr, ldr = residual.data_ptr(), _ld(residual, "residual")
-    with _on(device):
+    on = _on(device, stream)
+    with on as handle:
         made_out = out is None
         if made_out:
             out = torch.empty(rows, n, dtype=dtype, device=x.device)
@@ -192,13 +208,12 @@ def _forward(x, w, offsets, bias, residual, activation, save_preact, out, preact
                                  _ld(x, "x"), _ld(w, "w"), ldo, ldr, ldp)
         nbytes = capi.ccl_linear_workspace(d, grouped, False)
         ws = _workspace(nbytes, x.device)
-        pws, s = (ws.data_ptr() if nbytes else 0), _stream(stream, device)
+        pws = ws.data_ptr() if nbytes else 0
         if grouped:
-            capi.ccl_grouped_linear(d, po, px, pw, pb, pout, pp, pws, nbytes, s)
+            capi.ccl_grouped_linear(d, po, px, pw, pb, pout, pp, pws, nbytes, handle)
         else:
-            capi.ccl_linear(d, px, pw, pb, pr, pout, pp, pws, nbytes, s)
-        if stream is not None:
-            _own(stream, ws, out if made_out else None, preact if made_preact else None)
+            capi.ccl_linear(d, px, pw, pb, pr, pout, pp, pws, nbytes, handle)
+        on.give(out if made_out else None, preact if made_preact else None)
     return out if preact is None else (out, preact)
 
 
@@ -233,7 +248,8 @@ def _backward(dout, x, w, offsets, preact, activation, bias, need_dx, need_dw, s
             _refuse("the activation's gradient needs preact")
         _like(preact, "preact", (rows, n), dtype, device)
         pp, ldp = preact.data_ptr(), _ld(preact, "preact")
-    with _on(device):
+    on = _on(device, stream)
+    with on as handle:
         dx = torch.empty(rows, k, dtype=dtype, device=x.device) if need_dx else None
         dw = torch.empty(w.shape, dtype=dtype, device=x.device) if need_dw else None
         db = torch.empty(w.shape[:-1], dtype=dtype, device=x.device) if bias else None
@@ -243,13 +259,12 @@ def _backward(dout, x, w, offsets, preact, activation, bias, need_dx, need_dw, s
         nbytes = capi.ccl_linear_workspace(d, grouped, True)
         ws = _workspace(nbytes, x.device)
         tail = (pd, px, pw, pp, dx.data_ptr() if need_dx else 0, dw.data_ptr() if need_dw else 0,
-                db.data_ptr() if bias else 0, ws.data_ptr() if nbytes else 0, nbytes, _stream(stream, device))
+                db.data_ptr() if bias else 0, ws.data_ptr() if nbytes else 0, nbytes, handle)
         if grouped:
             capi.ccl_grouped_linear_backward(d, po, *tail)
         else:
             capi.ccl_linear_backward(d, *tail)
-        if stream is not None:
-            _own(stream, ws, dx, dw, db)
+        on.give(dx, dw, db)
     return [t for t in (dx, dw, db) if t is not None]
 
 
@@ -265,15 +280,15 @@ def expert_route(ids, experts, stream=None):
     pi = _packed(ids, "ids", ids.shape, torch.int32, device)
     tokens, choices = ids.shape
     nbytes = capi.ccl_expert_route_workspace(tokens, choices, experts)
-    with _on(device):
+    on = _on(device, stream)
+    with on as handle:
         offsets = torch.empty(experts + 1, dtype=torch.int32, device=ids.device)
         positions = torch.empty_like(ids)
         slots = torch.empty(tokens * choices, dtype=torch.int32, device=ids.device)
         ws = _workspace(nbytes, ids.device)
         capi.ccl_expert_route(pi, tokens, choices, experts, offsets.data_ptr(), positions.data_ptr(),
-                              slots.data_ptr(), ws.data_ptr() if nbytes else 0, nbytes, _stream(stream, device))
-        if stream is not None:
-            _own(stream, ws, offsets, positions, slots)
+                              slots.data_ptr(), ws.data_ptr() if nbytes else 0, nbytes, handle)
+        on.give(offsets, positions, slots)
     return offsets, positions, slots
 
 
@@ -287,7 +302,8 @@ def expert_dispatch(x, slots, choices, out=None, stream=None):
     device = _first(x, "x")
     tokens, width = x.shape
     ps = _packed(slots, "slots", (tokens * choices,), torch.int32, device)
-    with _on(device):
+    on = _on(device, stream)
+    with on as handle:
         made, ldo = out is None, 0
         if made:
             out = torch.empty(tokens * choices, width, dtype=x.dtype, device=x.device)
@@ -295,9 +311,9 @@ def expert_dispatch(x, slots, choices, out=None, stream=None):
             _like(out, "out", (tokens * choices, width), x.dtype, device)
             ldo = _ld(out, "out")
         capi.ccl_expert_dispatch(DTYPES[x.dtype], x.data_ptr(), _ld(x, "x"), ps, tokens, choices, width,
-                                 out.data_ptr(), ldo, _stream(stream, device))
-        if stream is not None and made:
-            _own(stream, out)
+                                 out.data_ptr(), ldo, handle)
+        if made:
+            on.give(out)
     return out
 
 
@@ -313,7 +329,8 @@ def expert_combine(h, positions, gates=None, out=None, stream=None):
     _like(h, "h", (tokens * choices, width), h.dtype, device)
     pp = _packed(positions, "positions", positions.shape, torch.int32, device)
     pg = _gates(gates, positions, device)
-    with _on(device):
+    on = _on(device, stream)
+    with on as handle:
         made, ldo = out is None, 0
         if made:
             out = torch.empty(tokens, width, dtype=h.dtype, device=h.device)
@@ -321,9 +338,9 @@ def expert_combine(h, positions, gates=None, out=None, stream=None):
             _like(out, "out", (tokens, width), h.dtype, device)
             ldo = _ld(out, "out")
         capi.ccl_expert_combine(DTYPES[h.dtype], h.data_ptr(), _ld(h, "h"), pp, pg, tokens, choices, width,
-                                out.data_ptr(), ldo, _stream(stream, device))
-        if stream is not None and made:
-            _own(stream, out)
+                                out.data_ptr(), ldo, handle)
+        if made:
+            on.give(out)
     return out
 
 
@@ -340,12 +357,12 @@ def expert_combine_backward(dout, h, positions, slots, gates=None, stream=None):
     pp = _packed(positions, "positions", positions.shape, torch.int32, device)
     ps = _packed(slots, "slots", (tokens * choices,), torch.int32, device)
     pg = _gates(gates, positions, device)
-    with _on(device):
+    on = _on(device, stream)
+    with on as handle:
         dh = torch.empty(tokens * choices, width, dtype=h.dtype, device=h.device)
         dgates = torch.empty(tokens, choices, dtype=torch.float32, device=h.device)
         capi.ccl_expert_combine_backward(DTYPES[h.dtype], dout.data_ptr(), _ld(dout, "dout"), h.data_ptr(),
                                          _ld(h, "h"), pp, ps, pg, tokens, choices, width, dh.data_ptr(), 0,
-                                         dgates.data_ptr(), _stream(stream, device))
-        if stream is not None:
-            _own(stream, dh, dgates)
+                                         dgates.data_ptr(), handle)
+        on.give(dh, dgates)
     return dh, dgates
