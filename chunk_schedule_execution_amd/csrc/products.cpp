@@ -365,12 +365,12 @@ int ccl_expert_combine_backward(int dtype, const void* dout, int64_t ld_dout, co
     ld_dh = stride_of(ld_dh, width, "ld_dh");
     if (count == 0 || (!dh && !dgates)) return CCL_OK;
     elements(elem_size(dtype), dout, "dout: null or misaligned");
+    elements(4, positions, "positions: null or misaligned");
     elements(4, slots, "slots: null or misaligned");
     if (gates) elements(4, gates, "gates: misaligned");
     if (dh) elements(elem_size(dtype), dh, "dh: misaligned");
     if (dgates) {
       elements(4, dgates, "dgates: misaligned");
-      elements(4, positions, "positions: null or misaligned");
       elements(elem_size(dtype), h, "h: null or misaligned");
     }
     std::string err;

@@ -645,10 +645,11 @@ int ccl_expert_dispatch(int dtype, const void* x, int64_t ld_x, const int32_t* s
 int ccl_expert_combine(int dtype, const void* h, int64_t ld_h, const int32_t* positions, const float* gates,
                        int64_t tokens, int choices, int64_t width, void* out, int64_t ld_out, void* stream);
 
-/* Gradients of the combine: dh[i] = gates[slots[i]] dout[slots[i] / choices] (zeros where
- * slots[i] is not a slot; gates NULL for ones) and dgates[slots[i]] = <h[i], dout[slots[i]
- * / choices]>, zero for a slot whose position is not a row. positions and slots are one
- * route's. dh or dgates (then h too) may be NULL. */
+/* Gradients of the combine: dh[positions[s]] = gates[s] dout[s / choices] for every slot s
+ * whose position is a row, zeros for the rows i whose slots[i] is not a slot (gates NULL for
+ * ones), and dgates[s] = <h[positions[s]], dout[s / choices]>, zero for a slot whose position
+ * is not a row. positions and slots are one route's, and both are always read. dh or dgates
+ * (then h too) may be NULL. */
 int ccl_expert_combine_backward(int dtype, const void* dout, int64_t ld_dout, const void* h, int64_t ld_h,
                                 const int32_t* positions, const int32_t* slots, const float* gates, int64_t tokens,
                                 int choices, int64_t width, void* dh, int64_t ld_dh, float* dgates, void* stream);
