@@ -223,10 +223,13 @@ __device__ inline TileJob find_job(const ProductArgs& g, ProductMode mode, unsig
   j.k_lo = uniform(int(k_lo));
   j.k_hi = uniform(int(k_hi));
   if (gridDim.y > 1) {  // this workgroup's share of the summed dimension, in whole steps
-    const int steps = uniform((j.k_hi - j.k_lo + Step - 1) / Step);
-    const int lo = j.k_lo + uniform(int(int64_t(steps) * blockIdx.y / gridDim.y)) * Step;
-    j.k_hi = min(j.k_hi, j.k_lo + uniform(int(int64_t(steps) * (blockIdx.y + 1) / gridDim.y)) * Step);
-    j.k_lo = lo;
+    // The steps end up to Step - 1 values past the range, which may be past 31 bits; times
+    // the 16 splits there are at most, their number stays below 2^31.
+    const unsigned range = max(0, j.k_hi - j.k_lo), steps = (range + Step - 1) / Step;
+    const unsigned lo = uniform(int(steps * blockIdx.y / gridDim.y)) * Step;
+    const unsigned hi = uniform(int(steps * (blockIdx.y + 1) / gridDim.y)) * Step;
+    j.k_hi = j.k_lo + int(min(range, hi));
+    j.k_lo += int(min(range, lo));
   }
   return j;
 }
@@ -353,7 +356,7 @@ __device__ inline void product_tiles(const ProductArgs& g, ProductMode mode, int
     const int64_t c = job.col + wn + (lane % kLanesPerRow) * 8;
     const int n = int(min(int64_t(8), g.n - c));
     // loads the bias: before the next tile's loads
-    Finish<T> finish(g, C, job.row + wm + lane / kLanesPerRow, kRowsPerPass, c, n, job.group, nothing);
+    Finish<T> finish(g, C, int64_t(job.row) + wm + lane / kLanesPerRow, kRowsPerPass, c, n, job.group, nothing);
     // the last reads of this tile's values were before the last barrier, so every wave may
     // load the next tile's
     begin(next);
@@ -367,14 +370,15 @@ __device__ inline void product_tiles(const ProductArgs& g, ProductMode mode, int
       __builtin_amdgcn_wave_barrier();
 #pragma nounroll
       for (int r = lane / kLanesPerRow; r < 16; r += kRowsPerPass, finish.next()) {
-        const int at = job.row + wm + i * 16 + r;
-        if (at >= job.m_end || n <= 0) continue;
+        // counted from the tile's first row: a last tile may end past 31 bits
+        const int in = wm + i * 16 + r;
+        if (in >= job.m_end - job.row || n <= 0) continue;
         const int chunk = (lane % kLanesPerRow) * 2;
         float v[8];
         *reinterpret_cast<f32x4*>(v) = *reinterpret_cast<const f32x4*>(stage + r * WTN + ((chunk ^ r) % kChunks) * 4);
         *reinterpret_cast<f32x4*>(v + 4) =
             *reinterpret_cast<const f32x4*>(stage + r * WTN + (((chunk + 1) ^ r) % kChunks) * 4);
-        if (g.partial) store8(partial_at(g, blockIdx.y, at, c), true, n, v);
+        if (g.partial) store8(partial_at(g, blockIdx.y, int64_t(job.row) + in, c), true, n, v);
         else finish.row(v);
       }
       __builtin_amdgcn_wave_barrier();
