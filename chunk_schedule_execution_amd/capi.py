@@ -121,6 +121,10 @@ class ccl_linear_desc(C.Structure):
                 ("ld_dx", C.c_int64), ("ld_dw", C.c_int64)]
 
 
+class ccl_product_info(C.Structure):
+    _fields_ = [("tile_rows", C.c_int32), ("tile_columns", C.c_int32), ("splits", C.c_int32), ("copies", C.c_int32)]
+
+
 ccl_tune_objective = C.CFUNCTYPE(C.c_double, C.POINTER(ccl_tune_point), C.c_void_p)
 
 
@@ -171,6 +175,7 @@ def _load():
         "ccl_stream_destroy": (C.c_int, [C.c_void_p]),
         "ccl_cu_probe": (C.c_int, [C.c_void_p, C.c_int, C.c_int, P(C.c_uint32)]),
         "ccl_linear_workspace": (C.c_int64, [P(ccl_linear_desc), C.c_int, C.c_int]),
+        "ccl_linear_info": (C.c_int, [P(ccl_linear_desc), C.c_int, C.c_int, P(ccl_product_info)]),
         "ccl_linear": (C.c_int, [P(ccl_linear_desc)] + [C.c_void_p] * 7 + [C.c_size_t, C.c_void_p]),
         "ccl_linear_backward": (C.c_int, [P(ccl_linear_desc)] + [C.c_void_p] * 8 + [C.c_size_t, C.c_void_p]),
         "ccl_grouped_linear": (C.c_int, [P(ccl_linear_desc)] + [C.c_void_p] * 7 + [C.c_size_t, C.c_void_p]),
@@ -199,7 +204,7 @@ EXPORTED = ("ccl_version", "ccl_error_string", "ccl_last_error_detail", "ccl_pla
             "ccl_plan_destroy", "ccl_plan_info", "ccl_plan_bytes", "ccl_plan_export", "ccl_plan_check",
             "ccl_plan_status", "ccl_plan_read_trace", "ccl_plan_link_busy", "ccl_tune_coordinate_descent", "ccl_tune",
             "ccl_copy_probe", "ccl_litmus_message_passing", "ccl_hop_probe", "ccl_stream_create_cu_masked",
-            "ccl_stream_destroy", "ccl_cu_probe", "ccl_linear_workspace", "ccl_linear", "ccl_linear_backward",
+            "ccl_stream_destroy", "ccl_cu_probe", "ccl_linear_workspace", "ccl_linear_info", "ccl_linear", "ccl_linear_backward",
             "ccl_grouped_linear", "ccl_grouped_linear_backward", "ccl_expert_route_workspace", "ccl_expert_route",
             "ccl_expert_dispatch", "ccl_expert_combine", "ccl_expert_combine_backward")
 
@@ -387,6 +392,13 @@ def ccl_linear_workspace(desc: ccl_linear_desc, grouped: bool, backward: bool) -
     if v < 0:
         _check(int(v), "ccl_linear_workspace")
     return int(v)
+
+
+def ccl_linear_info(desc: ccl_linear_desc, grouped: bool, backward: bool):
+    """[ccl_product_info] of a forward call, [dx's, dw's] of a backward call."""
+    out = (ccl_product_info * 2)()
+    _check(_lib.ccl_linear_info(C.byref(desc), int(bool(grouped)), int(bool(backward)), out), "ccl_linear_info")
+    return list(out)[:2 if backward else 1]
 
 
 def ccl_linear(desc: ccl_linear_desc, x: int, w: int, bias: int, residual: int, out: int, preact: int, workspace: int,

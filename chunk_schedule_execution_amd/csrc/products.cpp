@@ -135,6 +135,11 @@ int64_t workspace_bytes_of(const ccl_linear_desc& d, bool grouped, bool backward
   return backward ? backward_plan(d, grouped).total : forward_plan(d, grouped).bytes;
 }
 
+ccl_product_info info_of(const ProductPlan& p) {
+  const int edge = p.kind == kTile64 ? 64 : p.kind == kTile128 ? 128 : 256;
+  return {p.kind == kRows16 ? 16 : edge, p.kind == kRows16 ? 16 * p.columns : edge, p.splits, int(p.copy_a) + int(p.copy_b)};
+}
+
 void check_workspace(const void* ws, size_t have, int64_t need) {
   if (need == 0) return;
   if (!ws || int64_t(have) < need)
@@ -260,6 +265,21 @@ int64_t ccl_linear_workspace(const ccl_linear_desc* desc, int grouped, int backw
     return CCL_OK;
   });
   return rc ? rc : bytes;
+}
+
+int ccl_linear_info(const ccl_linear_desc* desc, int grouped, int backward, ccl_product_info* info) {
+  return api_guarded([&] {
+    const ccl_linear_desc d = checked(desc, grouped != 0);
+    require(info != nullptr, "null info");
+    if (backward) {
+      const BackwardPlan p = backward_plan(d, grouped != 0);
+      info[0] = info_of(p.dx);
+      info[1] = info_of(p.dw);
+    } else {
+      info[0] = info_of(forward_plan(d, grouped != 0));
+    }
+    return CCL_OK;
+  });
 }
 
 int ccl_linear(const ccl_linear_desc* desc, const void* x, const void* w, const void* bias, const void* residual,

@@ -583,6 +583,19 @@ typedef struct {
 int64_t ccl_linear_workspace(const ccl_linear_desc* desc, int grouped, int backward);
 
 /*
+ * How a call with this descriptor runs its products, from sizes, types and alignment
+ * alone: info[0] of a forward call; info[0] (dx) and info[1] (dw) of a backward call. Errors:
+ * those of the descriptor, INVALID_ARGUMENT (info is NULL).
+ */
+typedef struct {
+  int32_t tile_rows;    /* a workgroup's tile: 64, 128 or 256 rows and as many columns, or */
+  int32_t tile_columns; /* 16 rows and 16 or 32 columns in the kernel for few rows */
+  int32_t splits;       /* shares of the summed dimension; above 1 a second kernel adds them */
+  int32_t copies;       /* matrices first copied onto the 16-byte grid: 0 .. 2 */
+} ccl_product_info;
+int ccl_linear_info(const ccl_linear_desc* desc, int grouped, int backward, ccl_product_info* info);
+
+/*
  * out = act(z) + residual with z = x w^T + bias: x rows x in_features, w out_features x
  * in_features, bias out_features or NULL, residual rows x out_features or NULL, out rows
  * x out_features, preact NULL or rows x out_features (receives z). The activation sees z
