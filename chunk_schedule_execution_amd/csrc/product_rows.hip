@@ -7,12 +7,9 @@ namespace {
 
 template <typename T, int FN, int Deep>
 int go(const ProductArgs& g, const ProductPlan& plan, hipStream_t s, std::string* err) {
-  const int64_t slabs = (g.n + 16 * FN - 1) / (16 * FN), bands = (g.m + 15) / 16 + (g.offsets ? g.groups : 0);
-  if (bands * slabs > 0x7fffffff) {
-    *err = "product: more than 2^31 workgroups";
-    return CCL_ERR_INVALID_ARGUMENT;
-  }
-  const dim3 grid(unsigned(bands * slabs), plan.splits);
+  const int64_t slabs = (g.n + 16 * FN - 1) / (16 * FN);
+  // the plan has seen to it that a grid holds them
+  const dim3 grid(unsigned(rows16_workgroups(g.offsets ? kRaggedM : kPlain, g, FN)), plan.splits);
   if (plan.vec)
     hipLaunchKernelGGL((product_rows_kernel<T, FN, true, Deep>), grid, dim3(256), 0, s, g, int(slabs));
   else

@@ -54,6 +54,8 @@ struct ProductPlan {
 enum OperandGrid : int { kByStrides, kOffGrid, kPadded };
 ProductPlan plan_product(int dtype, bool a_by_k, bool b_by_k, ProductMode mode, const ProductArgs& args,
                          OperandGrid a_grid, OperandGrid b_grid);
+// The few-row kernel's grid, in its first dimension.
+int64_t rows16_workgroups(ProductMode mode, const ProductArgs& args, int columns);
 int launch_product(int dtype, bool a_by_k, bool b_by_k, ProductMode mode, const ProductArgs& args,
                    const ProductPlan& plan, void* workspace, void* stream, std::string* err);
 

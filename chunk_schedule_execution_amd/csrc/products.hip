@@ -261,7 +261,15 @@ void choose_tile(int dtype, ProductMode mode, const ProductArgs& g, ProductPlan&
   if (best == 0) p.kind = sizes[count - 1].kind;
 }
 
+// Workgroups of 256 threads that one dimension of a grid holds: fewer than 2^32 threads.
+constexpr int64_t kMaxWorkgroups = (int64_t(1) << 24) - 1;
+
 }  // namespace
+
+int64_t rows16_workgroups(ProductMode mode, const ProductArgs& g, int columns) {
+  const int64_t bands = (g.m + 15) / 16 + (mode == kPlain ? 0 : g.groups);
+  return bands * ((g.n + 16 * columns - 1) / (16 * columns));
+}
 
 ProductPlan plan_product(int dtype, bool a_by_k, bool b_by_k, ProductMode mode, const ProductArgs& g,
                          OperandGrid a_grid, OperandGrid b_grid) {
@@ -275,9 +283,11 @@ ProductPlan plan_product(int dtype, bool a_by_k, bool b_by_k, ProductMode mode, 
   // take 37 us and 45 in tiles of 64, 512 rows 57 and 65, 1 x 4096 x 16384 fp32 64 and 80, 4 x
   // 1024 x 1024 bf16 4.5 and 9. One large bf16 matrix the tiles read faster (1 x 4096 x 16384:
   // 32 us and 35). Weights off the 16-byte grid this kernel reads as they are, uncopied.
+  // Its grid has a workgroup for every tile of 16 rows, one more per group, and holds fewer
+  // than 2^32 threads; beyond that the tiles, whose grid does not grow, take the call.
   const int64_t mean = g.m / g.groups;
   const bool few = g.groups > 1 ? mean <= 8 : g.m <= 16;
-  if (!a_by_k && !b_by_k && mode != kRaggedK && few && up(g.m, 16) * up(g.n, 16) < (1 << 23) &&
+  if (!a_by_k && !b_by_k && mode != kRaggedK && few && rows16_workgroups(mode, g, 2) <= kMaxWorkgroups &&
       (dtype == CCL_F32 || g.groups > 1 || !on_a || !on_b || g.n * g.k * size <= (32 << 20))) {
     p.kind = kRows16;
     p.vec = on_a && on_b;

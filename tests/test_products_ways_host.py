@@ -37,3 +37,25 @@ def test_info_follows_the_alignment():
             assert capi.ccl_linear_info(d, False, False)[0].copies == copies
         d = capi.ccl_linear_desc(dtype=capi.CCL_BF16, rows=rows, in_features=1024, out_features=512)
         assert capi.ccl_linear_info(d, False, False)[0].copies == 0
+
+
+def few_row_workgroups(rows, n, experts, columns):
+    return ((rows + 15) // 16 + experts) * ((n + columns - 1) // columns)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_the_few_row_kernel_has_a_grid_that_holds_it(dtype):
+    """A workgroup of 256 threads per tile of 16 rows, one more per group, and per 16 or 32
+    columns; a grid's dimension holds fewer than 2^32 threads. Beyond it tiles are taken."""
+    few = many = 0
+    for experts in (0, 2, 64, 512, 2048, 4096):
+        for rows in (1, 16, 8 * max(1, experts)):
+            for n in (1, 4096, 65536, 1 << 18, (1 << 20) - 1, 1 << 20):
+                d = capi.ccl_linear_desc(W.TYPES[dtype], capi.CCL_ACT_RELU, rows, 8, n, experts, 0)
+                i = capi.ccl_linear_info(d, experts > 0, False)[0]
+                if i.tile_rows == 16:
+                    few += 1
+                    assert few_row_workgroups(rows, n, experts, i.tile_columns) * 256 < 1 << 32
+                elif experts and few_row_workgroups(rows, n, experts, 32) * 256 >= 1 << 32:
+                    many += 1
+    assert few and many
