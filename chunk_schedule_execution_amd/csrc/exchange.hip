@@ -11,13 +11,6 @@ namespace ccl {
 namespace prod {
 namespace {
 
-int hip_status(const char* what, std::string* err) {
-  const hipError_t e = hipGetLastError();
-  if (e == hipSuccess) return CCL_OK;
-  *err = std::string(what) + ": " + hipGetErrorString(e);
-  return CCL_ERR_HIP;
-}
-
 constexpr int kMaxExperts = 1024;
 
 // ---- routing ---------------------------------------------------------------------------

@@ -30,15 +30,6 @@ __device__ inline auto load_k(const T* row, int k, int k_end) {
   return v;
 }
 
-__device__ inline f32x4 multiply_rows(bf16x8 x, bf16x8 y, f32x4 acc) {
-  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, y, acc, 0, 0, 0);
-}
-__device__ inline f32x4 multiply_rows(f32x4 x, f32x4 y, f32x4 acc) {
-#pragma unroll
-  for (int q = 0; q < 4; ++q) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(x[q], y[q], acc, 0, 0, 0);
-  return acc;
-}
-
 // A workgroup computes 16 rows by 16 FN columns. Its four waves split the summed
 // dimension by lines of 128 bytes, every operand value goes straight from memory into the
 // registers of a matrix instruction (nothing is used twice within a workgroup, so LDS
@@ -54,7 +45,7 @@ __device__ inline void product_rows(const ProductArgs& g, int slabs) {
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int band = uniform(blockIdx.x / slabs);
   const int64_t col = int64_t(blockIdx.x - band * slabs) * (16 * FN);
-  const RowTile t = find_tile(g.offsets, g.groups, g.m, 16, band, true);
+  const RowTile t = find_tile(g.offsets, g.groups, g.m, 16, band);
   if (t.group < 0) return;
   const bool nothing = g.offsets && t.group == g.groups;
   const T* A = static_cast<const T*>(g.a);
@@ -88,7 +79,7 @@ __device__ inline void product_rows(const ProductArgs& g, int slabs) {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int j = 0; j < FN; ++j) acc[j] = multiply_rows(b[d][h][j], a[d][h], acc[j]);
+          for (int j = 0; j < FN; ++j) acc[j] = multiply(b[d][h][j], a[d][h], acc[j]);
     }
 #pragma unroll
     for (int j = 0; j < FN; ++j)

@@ -14,10 +14,7 @@ int go(const ProductArgs& g, const ProductPlan& plan, hipStream_t s, std::string
     hipLaunchKernelGGL((product_rows_kernel<T, FN, true, Deep>), grid, dim3(256), 0, s, g, int(slabs));
   else
     hipLaunchKernelGGL((product_rows_kernel<T, FN, false, Deep>), grid, dim3(256), 0, s, g, int(slabs));
-  const hipError_t e = hipGetLastError();
-  if (e == hipSuccess) return CCL_OK;
-  *err = std::string("product launch: ") + hipGetErrorString(e);
-  return CCL_ERR_HIP;
+  return hip_status("product launch", err);
 }
 
 template <typename T>

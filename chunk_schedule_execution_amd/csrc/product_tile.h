@@ -146,15 +146,6 @@ struct FragmentReader {
   }
 };
 
-__device__ inline f32x4 multiply(bf16x8 x, bf16x8 y, f32x4 acc) {
-  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, y, acc, 0, 0, 0);
-}
-__device__ inline f32x4 multiply(f32x4 x, f32x4 y, f32x4 acc) {
-#pragma unroll
-  for (int q = 0; q < 4; ++q) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(x[q], y[q], acc, 0, 0, 0);
-  return acc;
-}
-
 // All waves' reads of LDS before this point are done and their loads into LDS have arrived.
 __device__ inline void steps_arrived() {
   asm volatile("" ::: "memory");
@@ -210,7 +201,7 @@ __device__ inline TileJob find_job(const ProductArgs& g, ProductMode mode, unsig
     group_bounds(g.offsets, g.k, j.group, k_lo, k_hi);
   } else {
     place_tile<8>(id, tiles, tiles_n, band, column);
-    const RowTile t = find_tile(g.offsets, g.groups, g.m, BM, band, true);
+    const RowTile t = find_tile(g.offsets, g.groups, g.m, BM, band);
     j.group = uniform(t.group);
     row = t.row;
     m_end = t.end;
@@ -261,7 +252,7 @@ __device__ inline void product_tiles(const ProductArgs& g, ProductMode mode, int
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / WN * (BM / WM), wn = wave % WN * WTN;
   // groups leave some of the tiles unused: only those that exist are spread over the XCDs
-  const unsigned tiles = mode == kRaggedM ? unsigned(count_tiles(g.offsets, g.groups, g.m, BM, true)) * tiles_n : all;
+  const unsigned tiles = mode == kRaggedM ? unsigned(count_tiles(g.offsets, g.groups, g.m, BM)) * tiles_n : all;
 
   OperandTile<T, AByK, BM, Threads> ta;
   OperandTile<T, BByK, BN, Threads> tb;
@@ -416,10 +407,7 @@ int launch_tile(bool a_by_k, bool b_by_k, ProductMode mode, const ProductArgs& g
   if (a_by_k && b_by_k) go(product_tile_kernel<T, true, true, BM, BN, WM, WN>);
   else if (b_by_k) go(product_tile_kernel<T, false, true, BM, BN, WM, WN>);
   else go(product_tile_kernel<T, false, false, BM, BN, WM, WN>);
-  const hipError_t e = hipGetLastError();
-  if (e == hipSuccess) return CCL_OK;
-  *err = std::string("product launch: ") + hipGetErrorString(e);
-  return CCL_ERR_HIP;
+  return hip_status("product launch", err);
 }
 
 }  // namespace

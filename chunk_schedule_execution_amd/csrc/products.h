@@ -47,7 +47,7 @@ struct ProductPlan {
   bool vec = true;                   // kRows16: both operands lie on the 16-byte grid
   bool copy_a = false, copy_b = false;  // tiles: operands that are first copied onto that grid
   int64_t ld_a = 0, ld_b = 0;        // of the copies
-  int64_t at_a = 0, at_b = 0, at_partial = 0, bytes = 0;  // workspace layout
+  int64_t at_b = 0, at_partial = 0, bytes = 0;  // workspace layout: the copy of a, of b, the splits' sums
 };
 // Where an operand's stored rows lie: on the 16-byte grid if strides and lengths are whole
 // vectors; off it, its base pointer being unaligned; or on it with zeros up to the vector.

@@ -17,13 +17,6 @@ int launch_rows(int dtype, const ProductArgs& g, const ProductPlan& plan, hipStr
 
 namespace {
 
-int hip_status(const char* what, std::string* err) {
-  const hipError_t e = hipGetLastError();
-  if (e == hipSuccess) return CCL_OK;
-  *err = std::string(what) + ": " + hipGetErrorString(e);
-  return CCL_ERR_HIP;
-}
-
 // ---- operands off the 16-byte grid ------------------------------------------------------
 // Rows copied to a stride of whole vectors, zeros behind their end: one pass over the
 // operand, 5 us for the 1111 x 1001 of an odd product. Both operands in one launch.
@@ -62,7 +55,7 @@ constexpr int kJoinRows = 16;
 
 template <typename T>
 __global__ __launch_bounds__(256) void join_kernel(ProductArgs g, int splits) {
-  const RowTile t = find_tile(g.offsets, g.groups, g.m, kJoinRows, blockIdx.x, true);
+  const RowTile t = find_tile(g.offsets, g.groups, g.m, kJoinRows, blockIdx.x);
   const int64_t c = int64_t(blockIdx.y) * 256 + (threadIdx.x & 31) * 8;
   if (t.group < 0 || c >= g.n) return;
   const bool nothing = g.offsets && t.group == g.groups;
@@ -112,7 +105,7 @@ int slope_height(int64_t rows, int64_t n) {
 template <typename T>
 __global__ __launch_bounds__(256) void slope_kernel(SlopeArgs g, int height, bool vec_o, bool vec_p) {
   __shared__ float sums[kSlopeLanes][256];
-  const RowTile t = find_tile(g.offsets, g.groups, g.rows, height, blockIdx.x, true);
+  const RowTile t = find_tile(g.offsets, g.groups, g.rows, height, blockIdx.x);
   if (t.group < 0) return;
   const int64_t c = int64_t(blockIdx.y) * 256 + (threadIdx.x & 31) * 8;
   const int n = int(min(int64_t(8), g.n - c)), lane = threadIdx.x >> 5;
@@ -258,7 +251,6 @@ void choose_tile(int dtype, ProductMode mode, const ProductArgs& g, ProductPlan&
       }
     }
   }
-  if (best == 0) p.kind = sizes[count - 1].kind;
 }
 
 // Workgroups of 256 threads that one dimension of a grid holds: fewer than 2^32 threads.
@@ -320,8 +312,8 @@ int launch_product(int dtype, bool a_by_k, bool b_by_k, ProductMode mode, const 
   Regrid copy[2];
   int copies = 0;
   if (plan.copy_a) {
-    copy[copies++] = {g.a, ws + plan.at_a, g.lda, a_by_k ? g.k : g.m, a_by_k ? g.m : g.k, plan.ld_a};
-    g.a = ws + plan.at_a;
+    copy[copies++] = {g.a, ws, g.lda, a_by_k ? g.k : g.m, a_by_k ? g.m : g.k, plan.ld_a};
+    g.a = ws;
     g.lda = plan.ld_a;
   }
   if (plan.copy_b) {

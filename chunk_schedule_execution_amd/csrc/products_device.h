@@ -5,6 +5,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <string>
 
 #include "../../include/ccl.h"
 #include "products.h"
@@ -16,11 +17,29 @@ typedef __bf16 bf16;
 typedef bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
+// The status of the launches before it.
+inline int hip_status(const char* what, std::string* err) {
+  const hipError_t e = hipGetLastError();
+  if (e == hipSuccess) return CCL_OK;
+  *err = std::string(what) + ": " + hipGetErrorString(e);
+  return CCL_ERR_HIP;
+}
+
 __device__ inline float widen(bf16 v) { return float(v); }
 __device__ inline float widen(float v) { return v; }
 template <typename T>
 __device__ inline T narrow(float v) {
   return T(v);  // nearest-even
+}
+
+// One step of the summed dimension of a 16 x 16 tile: 32 values in bf16, 16 in fp32.
+__device__ inline f32x4 multiply(bf16x8 x, bf16x8 y, f32x4 acc) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, y, acc, 0, 0, 0);
+}
+__device__ inline f32x4 multiply(f32x4 x, f32x4 y, f32x4 acc) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(x[q], y[q], acc, 0, 0, 0);
+  return acc;
 }
 
 // exp(-v) and 1 / v by the hardware's own instructions (one fp32 step each).
@@ -108,52 +127,60 @@ struct RowTile {
   int64_t end;  // end of the group
 };
 
-// The tile-th tile of `height` rows when every group is cut into tiles of its own. Runs
-// on whole waves: lane l reads offset l, a running maximum makes the bounds monotone
-// (offset 0 counts as 0, values are clamped to [0, rows]), a prefix sum counts tiles.
-// With at most 64 groups that is one round of loads and 12 shuffles; more groups take a
-// round for every 64.
-__device__ inline RowTile find_tile(const int32_t* offsets, int groups, int64_t rows, int height, int tile,
-                                    bool with_rest) {
-  const int lane = here(threadIdx.x & 63);
-  if (offsets == nullptr) {
-    const int64_t row = int64_t(tile) * height;
-    return {row < rows ? 0 : -1, tile, row, rows};
-  }
-  int carry_tiles = 0, carry_max = 0;
-  const int last = with_rest ? groups : groups - 1;
-  for (int base = 0; base <= last; base += 64) {
+// The groups' bounds and tiles when every group is cut into tiles of `height` rows of its
+// own, 64 groups at a time on a whole wave: lane l reads offset base + l, a running maximum
+// makes the bounds monotone (offset 0 counts as 0, values are clamped to [0, rows]), a prefix
+// sum counts tiles. Group `groups` is the rows behind the last group. With at most 64 groups
+// that is one round of loads and 12 shuffles.
+struct GroupScan {
+  int lo = 0, hi = 0;        // this lane's group
+  int tiles = 0, upto = 0;   // its tiles; those up to and with its own
+  int tiles_before = 0, top = 0;  // of the rounds before
+
+  __device__ inline void round(const int32_t* offsets, int groups, int64_t rows, int height, int base, int lane) {
     const int e = base + lane;
-    int hi = 0;
-    if (e < groups)
-      hi = max(0, min(offsets[e + 1], int(rows)));
-    else
-      hi = int(rows);
+    hi = e < groups ? max(0, min(offsets[e + 1], int(rows))) : int(rows);
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
       const int v = __shfl_up(hi, d);
       if (lane >= d) hi = max(hi, v);
     }
-    hi = max(hi, carry_max);
-    int lo = __shfl_up(hi, 1);
-    if (lane == 0) lo = carry_max;
-    int tiles = e <= last ? int((int64_t(hi) - lo + height - 1) / height) : 0;
-    int upto = tiles;
+    hi = max(hi, top);
+    lo = __shfl_up(hi, 1);
+    if (lane == 0) lo = top;
+    tiles = e <= groups ? int((int64_t(hi) - lo + height - 1) / height) : 0;
+    upto = tiles;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
       const int v = __shfl_up(upto, d);
       if (lane >= d) upto += v;
     }
-    upto += carry_tiles;
-    const unsigned long long hit = __ballot(tile < upto);
+    upto += tiles_before;
+  }
+  // carries on to the next round
+  __device__ inline void carry() {
+    tiles_before = __builtin_amdgcn_readlane(upto, 63);
+    top = __builtin_amdgcn_readlane(hi, 63);
+  }
+};
+
+// The tile-th tile of `height` rows of the groups and the rows behind them.
+__device__ inline RowTile find_tile(const int32_t* offsets, int groups, int64_t rows, int height, int tile) {
+  const int lane = here(threadIdx.x & 63);
+  if (offsets == nullptr) {
+    const int64_t row = int64_t(tile) * height;
+    return {row < rows ? 0 : -1, tile, row, rows};
+  }
+  GroupScan s;
+  for (int base = 0; base <= groups; base += 64, s.carry()) {
+    s.round(offsets, groups, rows, height, base, lane);
+    const unsigned long long hit = __ballot(tile < s.upto);
     if (hit) {
       const int l = __ffsll(hit) - 1;
-      const int first = __builtin_amdgcn_readlane(upto - tiles, l);
-      const int64_t row = int64_t(__builtin_amdgcn_readlane(lo, l)) + int64_t(tile - first) * height;
-      return {base + l, tile, row, int64_t(__builtin_amdgcn_readlane(hi, l))};
+      const int first = __builtin_amdgcn_readlane(s.upto - s.tiles, l);
+      const int64_t row = int64_t(__builtin_amdgcn_readlane(s.lo, l)) + int64_t(tile - first) * height;
+      return {base + l, tile, row, int64_t(__builtin_amdgcn_readlane(s.hi, l))};
     }
-    carry_tiles = __builtin_amdgcn_readlane(upto, 63);
-    carry_max = __builtin_amdgcn_readlane(hi, 63);
   }
   return {-1, tile, 0, 0};
 }
@@ -176,28 +203,11 @@ __device__ inline void group_bounds(const int32_t* offsets, int64_t rows, int gr
 }
 
 // How many tiles find_tile knows.
-__device__ inline int count_tiles(const int32_t* offsets, int groups, int64_t rows, int height, bool with_rest) {
+__device__ inline int count_tiles(const int32_t* offsets, int groups, int64_t rows, int height) {
   if (offsets == nullptr) return int((rows + height - 1) / height);
-  const int lane = threadIdx.x & 63, last = with_rest ? groups : groups - 1;
-  int total = 0, carry_max = 0;
-  for (int base = 0; base <= last; base += 64) {
-    const int e = base + lane;
-    int hi = e < groups ? max(0, min(offsets[e + 1], int(rows))) : int(rows);
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int v = __shfl_up(hi, d);
-      if (lane >= d) hi = max(hi, v);
-    }
-    hi = max(hi, carry_max);
-    int lo = __shfl_up(hi, 1);
-    if (lane == 0) lo = carry_max;
-    int tiles = e <= last ? int((int64_t(hi) - lo + height - 1) / height) : 0;
-#pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) tiles += __shfl_xor(tiles, d);
-    total += uniform(tiles);
-    carry_max = __builtin_amdgcn_readlane(hi, 63);
-  }
-  return total;
+  GroupScan s;
+  for (int base = 0; base <= groups; base += 64, s.carry()) s.round(offsets, groups, rows, height, base, threadIdx.x & 63);
+  return uniform(s.tiles_before);
 }
 
 // The numbers of a group's tiles of `height` rows, [first, last).
@@ -208,34 +218,14 @@ __device__ inline void group_tiles(const int32_t* offsets, int groups, int64_t r
     last = (rows + height - 1) / height;
     return;
   }
-  const int lane = threadIdx.x & 63;
-  int carry_tiles = 0, carry_max = 0;
-  for (int base = 0; base <= group; base += 64) {
-    const int e = base + lane;
-    int hi = e < groups ? max(0, min(offsets[e + 1], int(rows))) : 0;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int v = __shfl_up(hi, d);
-      if (lane >= d) hi = max(hi, v);
-    }
-    hi = max(hi, carry_max);
-    int lo = __shfl_up(hi, 1);
-    if (lane == 0) lo = carry_max;
-    const int tiles = int((int64_t(hi) - lo + height - 1) / height);
-    int upto = tiles;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int v = __shfl_up(upto, d);
-      if (lane >= d) upto += v;
-    }
-    upto += carry_tiles;
-    if (group < base + 64) {
-      last = __builtin_amdgcn_readlane(upto, group - base);
-      first = last - __builtin_amdgcn_readlane(tiles, group - base);
-    }
-    carry_tiles = __builtin_amdgcn_readlane(upto, 63);
-    carry_max = __builtin_amdgcn_readlane(hi, 63);
+  GroupScan s;
+  int base = 0;
+  for (;; base += 64, s.carry()) {
+    s.round(offsets, groups, rows, height, base, threadIdx.x & 63);
+    if (group < base + 64) break;
   }
+  last = __builtin_amdgcn_readlane(s.upto, group - base);
+  first = last - __builtin_amdgcn_readlane(s.tiles, group - base);
 }
 
 // ---- results -----------------------------------------------------------------------------
