@@ -1,8 +1,9 @@
 """Build libccl.so in-tree with hipcc for gfx950.
 
 One shared library holds the host compiler, the plan runtime, the C entry points, the
-executor kernel and the kernels of the products and the row exchange. Host sources are plain C++17; the kernel source is HIP. Every
-file is compiled with packed-fp32 instructions disabled.
+executor kernel, and the kernels of the products, the row exchange and the layer's operators
+around them. Host sources are plain C++17; the kernel source is HIP. Every file is compiled
+with packed-fp32 instructions disabled.
 """
 
 from __future__ import annotations
@@ -19,9 +20,10 @@ LIBDIR = os.path.join(HERE, "lib")
 LIB = os.path.join(LIBDIR, "libccl.so")
 BUILD = os.path.join(ROOT, "_build")
 
-HOST_SOURCES = ["compiler.cpp", "simulate.cpp", "capi.cpp", "tune.cpp", "specialize.cpp", "products.cpp"]
+HOST_SOURCES = ["compiler.cpp", "simulate.cpp", "capi.cpp", "tune.cpp", "specialize.cpp", "products.cpp", "layers.cpp"]
 DEVICE_SOURCES = ["executor.hip", "static_scratch.hip", "hop_probe.hip", "products.hip", "product_tile_bf16.hip",
-                  "product_tile_f32.hip", "product_rows.hip", "exchange.hip"]
+                  "product_tile_f32.hip", "product_rows.hip", "exchange.hip", "select.hip", "norm.hip", "loss.hip",
+                  "loss_tile_bf16.hip", "loss_tile_f32.hip"]
 ARCH = "gfx950"
 COMMON = ["-O3", "-std=c++17", "-fPIC", "-Wall", "-Wno-unused-result", "-I", os.path.join(ROOT, "include"), "-I", "/opt/rocm/include"]
 DEVICE_FLAGS = [f"--offload-arch={ARCH}", "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",

@@ -46,6 +46,7 @@ CCL_I_RECV, CCL_I_SRCB, CCL_I_DSTA, CCL_I_SEND, CCL_I_LOCAL_IN = 0x1, 0x2, 0x4, 
 CCL_I_SKIP, CCL_I_NOFLAG = 0x20, 0x40
 CCL_ACT_NONE, CCL_ACT_RELU, CCL_ACT_GELU, CCL_ACT_GELU_TANH, CCL_ACT_SILU = range(5)
 CCL_LINEAR_UNALIGNED = 0x1
+CCL_SCORE_SOFTMAX, CCL_SCORE_SIGMOID = range(2)
 
 
 class ccl_chunk_op(C.Structure):
@@ -125,6 +126,24 @@ class ccl_product_info(C.Structure):
     _fields_ = [("tile_rows", C.c_int32), ("tile_columns", C.c_int32), ("splits", C.c_int32), ("copies", C.c_int32)]
 
 
+class ccl_select_desc(C.Structure):
+    _fields_ = [("dtype", C.c_int32), ("score", C.c_int32), ("tokens", C.c_int64), ("experts", C.c_int32),
+                ("choices", C.c_int32), ("groups", C.c_int32), ("kept_groups", C.c_int32), ("group_best", C.c_int32),
+                ("renormalise", C.c_int32), ("scale", C.c_float), ("ld_logits", C.c_int64), ("ld_dlogits", C.c_int64)]
+
+
+class ccl_norm_desc(C.Structure):
+    _fields_ = [("dtype", C.c_int32), ("eps", C.c_float), ("rows", C.c_int64), ("width", C.c_int64),
+                ("ld_x", C.c_int64), ("ld_residual", C.c_int64), ("ld_out", C.c_int64), ("ld_total", C.c_int64),
+                ("ld_dtotal", C.c_int64), ("ld_dx", C.c_int64)]
+
+
+class ccl_cross_entropy_desc(C.Structure):
+    _fields_ = [("dtype", C.c_int32), ("flags", C.c_uint32), ("rows", C.c_int64), ("in_features", C.c_int64),
+                ("vocabulary", C.c_int64), ("first", C.c_int64), ("ld_x", C.c_int64), ("ld_w", C.c_int64),
+                ("ld_dx", C.c_int64), ("ld_dw", C.c_int64)]
+
+
 ccl_tune_objective = C.CFUNCTYPE(C.c_double, C.POINTER(ccl_tune_point), C.c_void_p)
 
 
@@ -190,6 +209,17 @@ def _load():
         "ccl_expert_combine_backward": (C.c_int, [C.c_int, C.c_void_p, C.c_int64, C.c_void_p, C.c_int64, C.c_void_p,
                                                   C.c_void_p, C.c_void_p, C.c_int64, C.c_int, C.c_int64, C.c_void_p,
                                                   C.c_int64, C.c_void_p, C.c_void_p]),
+        "ccl_expert_select": (C.c_int, [P(ccl_select_desc)] + [C.c_void_p] * 5),
+        "ccl_expert_select_backward": (C.c_int, [P(ccl_select_desc)] + [C.c_void_p] * 5),
+        "ccl_layer_norm": (C.c_int, [P(ccl_norm_desc)] + [C.c_void_p] * 9),
+        "ccl_layer_norm_backward_workspace": (C.c_int64, [P(ccl_norm_desc)]),
+        "ccl_layer_norm_backward": (C.c_int, [P(ccl_norm_desc)] + [C.c_void_p] * 10 + [C.c_size_t, C.c_void_p]),
+        "ccl_linear_cross_entropy_workspace": (C.c_int64, [P(ccl_cross_entropy_desc), C.c_int]),
+        "ccl_linear_cross_entropy": (C.c_int, [P(ccl_cross_entropy_desc)] + [C.c_void_p] * 7 +
+                                     [C.c_size_t, C.c_void_p]),
+        "ccl_linear_cross_entropy_backward": (C.c_int, [P(ccl_cross_entropy_desc)] + [C.c_void_p] * 8 +
+                                              [C.c_size_t, C.c_void_p]),
+        "ccl_cross_entropy_join": (C.c_int, [C.c_int, C.c_int64] + [C.c_void_p] * 6),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -206,7 +236,10 @@ EXPORTED = ("ccl_version", "ccl_error_string", "ccl_last_error_detail", "ccl_pla
             "ccl_copy_probe", "ccl_litmus_message_passing", "ccl_hop_probe", "ccl_stream_create_cu_masked",
             "ccl_stream_destroy", "ccl_cu_probe", "ccl_linear_workspace", "ccl_linear_info", "ccl_linear", "ccl_linear_backward",
             "ccl_grouped_linear", "ccl_grouped_linear_backward", "ccl_expert_route_workspace", "ccl_expert_route",
-            "ccl_expert_dispatch", "ccl_expert_combine", "ccl_expert_combine_backward")
+            "ccl_expert_dispatch", "ccl_expert_combine", "ccl_expert_combine_backward", "ccl_expert_select",
+            "ccl_expert_select_backward", "ccl_layer_norm", "ccl_layer_norm_backward_workspace",
+            "ccl_layer_norm_backward", "ccl_linear_cross_entropy_workspace", "ccl_linear_cross_entropy",
+            "ccl_linear_cross_entropy_backward", "ccl_cross_entropy_join")
 
 
 def lib():
@@ -455,3 +488,59 @@ def ccl_expert_combine_backward(dtype: int, dout: int, ld_dout: int, h: int, ld_
                                 stream: int = 0) -> None:
     _check(_lib.ccl_expert_combine_backward(dtype, dout, ld_dout, h, ld_h, positions, slots, gates, tokens, choices,
                                             width, dh, ld_dh, dgates, stream), "ccl_expert_combine_backward")
+
+
+# ---- the layer's operators around the products ------------------------------------------
+def ccl_expert_select(desc: ccl_select_desc, logits: int, bias: int, ids: int, gates: int, stream: int = 0) -> None:
+    _check(_lib.ccl_expert_select(C.byref(desc), logits, bias, ids, gates, stream), "ccl_expert_select")
+
+
+def ccl_expert_select_backward(desc: ccl_select_desc, dgates: int, logits: int, ids: int, dlogits: int,
+                               stream: int = 0) -> None:
+    _check(_lib.ccl_expert_select_backward(C.byref(desc), dgates, logits, ids, dlogits, stream),
+           "ccl_expert_select_backward")
+
+
+def ccl_layer_norm(desc: ccl_norm_desc, x: int, residual: int, weight: int, bias: int, out: int, total: int, mean: int,
+                   rstd: int, stream: int = 0) -> None:
+    _check(_lib.ccl_layer_norm(C.byref(desc), x, residual, weight, bias, out, total, mean, rstd, stream),
+           "ccl_layer_norm")
+
+
+def ccl_layer_norm_backward_workspace(desc: ccl_norm_desc) -> int:
+    v = _lib.ccl_layer_norm_backward_workspace(C.byref(desc))
+    if v < 0:
+        _check(int(v), "ccl_layer_norm_backward_workspace")
+    return int(v)
+
+
+def ccl_layer_norm_backward(desc: ccl_norm_desc, dout: int, x: int, mean: int, rstd: int, weight: int, dtotal: int,
+                            dx: int, dweight: int, dbias: int, workspace: int, workspace_bytes: int,
+                            stream: int = 0) -> None:
+    _check(_lib.ccl_layer_norm_backward(C.byref(desc), dout, x, mean, rstd, weight, dtotal, dx, dweight, dbias,
+                                        workspace, workspace_bytes, stream), "ccl_layer_norm_backward")
+
+
+def ccl_linear_cross_entropy_workspace(desc: ccl_cross_entropy_desc, backward: bool) -> int:
+    v = _lib.ccl_linear_cross_entropy_workspace(C.byref(desc), int(bool(backward)))
+    if v < 0:
+        _check(int(v), "ccl_linear_cross_entropy_workspace")
+    return int(v)
+
+
+def ccl_linear_cross_entropy(desc: ccl_cross_entropy_desc, x: int, w: int, targets: int, loss: int, lse: int,
+                             picked: int, workspace: int, workspace_bytes: int, stream: int = 0) -> None:
+    _check(_lib.ccl_linear_cross_entropy(C.byref(desc), x, w, targets, loss, lse, picked, workspace, workspace_bytes,
+                                         stream), "ccl_linear_cross_entropy")
+
+
+def ccl_linear_cross_entropy_backward(desc: ccl_cross_entropy_desc, dloss: int, x: int, w: int, targets: int, lse: int,
+                                      dx: int, dw: int, workspace: int, workspace_bytes: int, stream: int = 0) -> None:
+    _check(_lib.ccl_linear_cross_entropy_backward(C.byref(desc), dloss, x, w, targets, lse, dx, dw, workspace,
+                                                  workspace_bytes, stream), "ccl_linear_cross_entropy_backward")
+
+
+def ccl_cross_entropy_join(shards: int, rows: int, lse_parts: int, picked_parts: int, targets: int, loss: int,
+                           lse: int, stream: int = 0) -> None:
+    _check(_lib.ccl_cross_entropy_join(shards, rows, lse_parts, picked_parts, targets, loss, lse, stream),
+           "ccl_cross_entropy_join")

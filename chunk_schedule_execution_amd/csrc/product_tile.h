@@ -225,6 +225,23 @@ __device__ inline TileJob find_job(const ProductArgs& g, ProductMode mode, unsig
   return j;
 }
 
+// The usual end of a tile: bias, activation, residual and stores, or the splits' sums.
+struct Results {
+  static constexpr bool kTakes = false, kAdds = false;
+  template <int FM>
+  struct Rows {
+    __device__ inline void load(const Results&, const ProductArgs&, const TileJob&, int) {}
+  };
+  template <int FM, int FN>
+  __device__ inline void change(f32x4 (&)[FM][FN], const Rows<FM>&, const ProductArgs&, const TileJob&, int) const {}
+  __device__ inline int64_t columns(const ProductArgs& g) const { return g.n; }
+};
+// Sums that are added onto those that an earlier part of the summed dimension left in
+// `partial`.
+struct AddedSums : Results {
+  static constexpr bool kAdds = true;
+};
+
 // BM x BN values per tile, WM x WN waves, each (BM / WM) x (BN / WN) by matrix instructions
 // of 16 x 16. Two LDS buffers, one barrier per step. A workgroup computes tile after tile:
 // the loads of a tile's first two steps start before the results of the tile before it are
@@ -238,8 +255,12 @@ __device__ inline TileJob find_job(const ProductArgs& g, ProductMode mode, unsig
 // unit's LDS. Lost against this: matrix instructions of 32 x 32 (810 us), two workgroups of
 // 256 x 128 per unit on half steps (as much matrix work, but 1.5 times the loads: 990 us),
 // four waves of 128 x 128 (registers spill).
-template <typename T, bool AByK, bool BByK, int BM, int BN, int WM, int WN>
-__device__ inline void product_tiles(const ProductArgs& g, ProductMode mode, int tiles_m, int tiles_n, unsigned all) {
+//
+// What becomes of a tile is End's: it may read what it needs of the tile's rows (`rows`),
+// change the sums in registers, or take them and leave no results.
+template <typename T, bool AByK, bool BByK, int BM, int BN, int WM, int WN, class End>
+__device__ inline void product_tiles(const ProductArgs& g, const End& ending, ProductMode mode, int tiles_m, int tiles_n,
+                                     unsigned all) {
   constexpr int Threads = WM * WN * 64, FM = BM / WM / 16, FN = BN / WN / 16;
   constexpr int kStep = 128 / int(sizeof(T));  // also the values per row of a stored tile
   constexpr int WTN = BN / WN;                 // columns of a wave
@@ -345,12 +366,20 @@ __device__ inline void product_tiles(const ProductArgs& g, ProductMode mode, int
     const bool nothing = mode == kRaggedM && job.group == g.groups;
     T* const C = static_cast<T*>(g.c) + (mode == kRaggedK ? job.group * g.c_stride : 0);
     const int64_t c = job.col + wn + (lane % kLanesPerRow) * 8;
-    const int n = int(min(int64_t(8), g.n - c));
+    const int n = int(min(int64_t(8), ending.columns(g) - c));
     // loads the bias: before the next tile's loads
     Finish<T> finish(g, C, int64_t(job.row) + wm + lane / kLanesPerRow, kRowsPerPass, c, n, job.group, nothing);
+    typename End::template Rows<FM> rows;
+    rows.load(ending, g, job, wm);
     // the last reads of this tile's values were before the last barrier, so every wave may
     // load the next tile's
     begin(next);
+    if constexpr (End::kTakes) {
+      ending.take(acc, rows, g, job, wm, wn);
+      job = next;
+      continue;
+    }
+    ending.change(acc, rows, g, job, wn);
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
 #pragma unroll
@@ -369,8 +398,18 @@ __device__ inline void product_tiles(const ProductArgs& g, ProductMode mode, int
         *reinterpret_cast<f32x4*>(v) = *reinterpret_cast<const f32x4*>(stage + r * WTN + ((chunk ^ r) % kChunks) * 4);
         *reinterpret_cast<f32x4*>(v + 4) =
             *reinterpret_cast<const f32x4*>(stage + r * WTN + (((chunk + 1) ^ r) % kChunks) * 4);
-        if (g.partial) store8(partial_at(g, blockIdx.y, int64_t(job.row) + in, c), true, n, v);
-        else finish.row(v);
+        if constexpr (End::kAdds) {
+          float* const sums = partial_at(g, blockIdx.y, int64_t(job.row) + in, c);
+          float before[8];
+          load8(sums, true, n, before);
+#pragma unroll
+          for (int q = 0; q < 8; ++q) v[q] += before[q];
+          store8(sums, true, n, v);
+        } else if (g.partial) {
+          store8(partial_at(g, blockIdx.y, int64_t(job.row) + in, c), true, n, v);
+        } else {
+          finish.row(v);
+        }
       }
       __builtin_amdgcn_wave_barrier();
     }
@@ -379,15 +418,15 @@ __device__ inline void product_tiles(const ProductArgs& g, ProductMode mode, int
 }
 
 // Two waves per SIMD: half of the registers each.
-template <typename T, bool AByK, bool BByK, int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__(WM* WN * 64, 2) void product_tile_kernel(ProductArgs g, ProductMode mode, int tiles_m,
-                                                                      int tiles_n, unsigned tiles) {
-  product_tiles<T, AByK, BByK, BM, BN, WM, WN>(g, mode, tiles_m, tiles_n, tiles);
+template <typename T, bool AByK, bool BByK, int BM, int BN, int WM, int WN, class End>
+__global__ __launch_bounds__(WM* WN * 64, 2) void product_tile_kernel(ProductArgs g, End ending, ProductMode mode,
+                                                                      int tiles_m, int tiles_n, unsigned tiles) {
+  product_tiles<T, AByK, BByK, BM, BN, WM, WN>(g, ending, mode, tiles_m, tiles_n, tiles);
 }
 
-template <typename T, int BM, int BN, int WM, int WN>
-int launch_tile(bool a_by_k, bool b_by_k, ProductMode mode, const ProductArgs& g, int splits, hipStream_t s,
-                std::string* err) {
+template <typename T, bool AByK, bool BByK, int BM, int BN, int WM, int WN, class End>
+int launch_tile_as(ProductMode mode, const ProductArgs& g, const End& ending, int splits, hipStream_t s,
+                   std::string* err) {
   constexpr int kUnits = 256, kXcds = 8;
   constexpr int kResident = 163840 / ((BM + BN) * 256 + WM * BN * 64);  // by LDS
   const int64_t tiles_n = (g.n + BN - 1) / BN, tiles_m = (g.m + BM - 1) / BM;
@@ -400,14 +439,17 @@ int launch_tile(bool a_by_k, bool b_by_k, ProductMode mode, const ProductArgs& g
   if (tiles == 0) return CCL_OK;
   // as many workgroups as are resident at a time, a multiple of the XCDs
   const int64_t grid = std::min<int64_t>(tiles, std::max<int64_t>(kXcds, kUnits * kResident / splits / kXcds * kXcds));
-  auto go = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, dim3(unsigned(grid), splits), dim3(WM * WN * 64), 0, s, g, mode, int(tiles_m), int(tiles_n),
-                       unsigned(tiles));
-  };
-  if (a_by_k && b_by_k) go(product_tile_kernel<T, true, true, BM, BN, WM, WN>);
-  else if (b_by_k) go(product_tile_kernel<T, false, true, BM, BN, WM, WN>);
-  else go(product_tile_kernel<T, false, false, BM, BN, WM, WN>);
+  hipLaunchKernelGGL((product_tile_kernel<T, AByK, BByK, BM, BN, WM, WN, End>), dim3(unsigned(grid), splits),
+                     dim3(WM * WN * 64), 0, s, g, ending, mode, int(tiles_m), int(tiles_n), unsigned(tiles));
   return hip_status("product launch", err);
+}
+
+template <typename T, int BM, int BN, int WM, int WN>
+int launch_tile(bool a_by_k, bool b_by_k, ProductMode mode, const ProductArgs& g, int splits, hipStream_t s,
+                std::string* err) {
+  if (a_by_k && b_by_k) return launch_tile_as<T, true, true, BM, BN, WM, WN>(mode, g, Results(), splits, s, err);
+  if (b_by_k) return launch_tile_as<T, false, true, BM, BN, WM, WN>(mode, g, Results(), splits, s, err);
+  return launch_tile_as<T, false, false, BM, BN, WM, WN>(mode, g, Results(), splits, s, err);
 }
 
 }  // namespace

@@ -5,29 +5,11 @@
 #include <algorithm>
 #include <string>
 
-#include "ccl_internal.h"
+#include "args.h"
 
 using namespace ccl;
 
 namespace {
-
-void require(bool ok, const char* what) {
-  if (!ok) fail(CCL_ERR_INVALID_ARGUMENT, what);
-}
-
-constexpr int64_t kMaxFeatures = int64_t(1) << 20, kMaxLd = int64_t(1) << 22;
-
-int elem_size(int dtype) {
-  if (dtype == CCL_F32) return 4;
-  if (dtype == CCL_BF16) return 2;
-  fail(CCL_ERR_UNSUPPORTED, "products take fp32 and bf16");
-}
-
-int64_t stride_of(int64_t ld, int64_t width, const char* name) {
-  if (ld == 0) return width;
-  if (ld < width || ld > kMaxLd) fail(CCL_ERR_INVALID_ARGUMENT, std::string(name) + ": a row stride below the row's length or above 2^22");
-  return ld;
-}
 
 // A descriptor with its strides filled in.
 ccl_linear_desc checked(const ccl_linear_desc* d, bool grouped) {
@@ -58,8 +40,6 @@ void aligned(const ccl_linear_desc& d, const void* p, const char* name) {
   if (!(d.flags & CCL_LINEAR_UNALIGNED) && a % 16)
     fail(CCL_ERR_INVALID_ARGUMENT, std::string(name) + ": not 16-byte aligned; set CCL_LINEAR_UNALIGNED");
 }
-
-int64_t align16(int64_t bytes) { return (bytes + 15) / 16 * 16; }
 
 // The products of a call, without pointers where only sizes are asked for.
 ProductArgs forward_args(const ccl_linear_desc& d) {
@@ -138,17 +118,6 @@ int64_t workspace_bytes_of(const ccl_linear_desc& d, bool grouped, bool backward
 ccl_product_info info_of(const ProductPlan& p) {
   const int edge = p.kind == kTile64 ? 64 : p.kind == kTile128 ? 128 : 256;
   return {p.kind == kRows16 ? 16 : edge, p.kind == kRows16 ? 16 * p.columns : edge, p.splits, int(p.copy_a) + int(p.copy_b)};
-}
-
-void check_workspace(const void* ws, size_t have, int64_t need) {
-  if (need == 0) return;
-  if (!ws || int64_t(have) < need)
-    fail(CCL_ERR_INVALID_ARGUMENT, "workspace: " + std::to_string(need) + " bytes needed, " + std::to_string(have) + " given");
-  require(reinterpret_cast<uintptr_t>(ws) % 16 == 0, "workspace: not 16-byte aligned");
-}
-
-void launched(int rc, const std::string& err) {
-  if (rc) fail(rc, err);
 }
 
 int forward(const ccl_linear_desc* desc, bool grouped, const int32_t* offsets, const void* x, const void* w,
@@ -249,11 +218,6 @@ int64_t exchange_checked(int dtype, int64_t tokens, int choices, int64_t width) 
   require(width >= 1 && width <= kMaxFeatures, "width: 1 .. 2^20");
   return tokens * choices;
 }
-void elements(int size, const void* p, const char* name) {
-  require(p != nullptr, name);
-  require(reinterpret_cast<uintptr_t>(p) % size == 0, name);
-}
-
 }  // namespace
 
 extern "C" {

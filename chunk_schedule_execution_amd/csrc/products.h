@@ -59,6 +59,18 @@ int64_t rows16_workgroups(ProductMode mode, const ProductArgs& args, int columns
 int launch_product(int dtype, bool a_by_k, bool b_by_k, ProductMode mode, const ProductArgs& args,
                    const ProductPlan& plan, void* workspace, void* stream, std::string* err);
 
+// The tile that a product of these sizes takes when its sums are not split.
+ProductKind unsplit_tile(int dtype, const ProductArgs& args);
+// Rows copied to a stride of whole 16-byte vectors, zeros behind their end.
+struct Regrid {
+  const void* src = nullptr;
+  void* dst = nullptr;
+  int64_t ld = 0, rows = 0, len = 0, ld_dst = 0;
+};
+int launch_regrid(int dtype, const Regrid& first, const Regrid& second, void* stream, std::string* err);
+// The results of a product from its splits' sums in args.partial.
+int launch_join(int dtype, const ProductArgs& args, int splits, void* stream, std::string* err);
+
 // dz = dout act'(preact) (skipped when dz is NULL; zeros behind a row up to ldz) and its
 // column sums by group (skipped when dbias is NULL). partial: fp32, slope_tiles() x n.
 struct SlopeArgs {

@@ -18,13 +18,8 @@ int launch_rows(int dtype, const ProductArgs& g, const ProductPlan& plan, hipStr
 namespace {
 
 // ---- operands off the 16-byte grid ------------------------------------------------------
-// Rows copied to a stride of whole vectors, zeros behind their end: one pass over the
-// operand, 5 us for the 1111 x 1001 of an odd product. Both operands in one launch.
-struct Regrid {
-  const void* src = nullptr;
-  void* dst = nullptr;
-  int64_t ld = 0, rows = 0, len = 0, ld_dst = 0;
-};
+// One pass over the operand, 5 us for the 1111 x 1001 of an odd product. Both operands in one
+// launch.
 
 template <typename T>
 __global__ __launch_bounds__(256) void regrid_kernel(Regrid first, Regrid second) {
@@ -212,7 +207,7 @@ namespace {
 // read at 5.6 TB/s at best, and slower by few workgroups, whose two steps in flight are too
 // little: 32 x 4096 x 16384 in 64s takes 54 us unsplit (one workgroup per unit), 42 in 2
 // splits and 36 in 4.
-void choose_tile(int dtype, ProductMode mode, const ProductArgs& g, ProductPlan& p) {
+void choose_tile(int dtype, ProductMode mode, const ProductArgs& g, int most_splits, ProductPlan& p) {
   struct Size {
     ProductKind kind;
     int edge, resident;
@@ -236,7 +231,7 @@ void choose_tile(int dtype, ProductMode mode, const ProductArgs& g, ProductPlan&
                                                           : double(up(g.m, z.edge));
     const double tiles = std::max(1.0, bands) * double(up(g.n, z.edge)) * (mode == kRaggedK ? g.groups : 1);
     for (int splits : {1, 2, 3, 4, 6, 8, 12, 16}) {
-      if (splits > 1 && (mode == kRaggedK || steps < 4 * splits)) break;
+      if (splits > most_splits || (splits > 1 && (mode == kRaggedK || steps < 4 * splits))) break;
       const int64_t each = int64_t(std::ceil(tiles * splits / kUnits));  // workgroups per compute unit
       auto step = [&](int64_t n) { return z.resident == 1 || n <= 1 ? z.alone * n : z.alone + (z.full - z.alone) * (n - 1) / (z.resident - 1); };
       const double rounds = double(each / z.resident);
@@ -288,7 +283,7 @@ ProductPlan plan_product(int dtype, bool a_by_k, bool b_by_k, ProductMode mode, 
     const int64_t wgs = std::max<int64_t>(1, bands * up(g.n, 16 * p.columns));
     p.splits = int(std::max<int64_t>(1, std::min<int64_t>(512 / wgs, g.k * size / 4096)));
   } else {
-    choose_tile(dtype, mode, g, p);
+    choose_tile(dtype, mode, g, 16, p);
     p.copy_a = !on_a;
     p.copy_b = !on_b;
     p.ld_a = up(a_by_k ? g.m : g.k, v) * v;
@@ -301,6 +296,20 @@ ProductPlan plan_product(int dtype, bool a_by_k, bool b_by_k, ProductMode mode, 
   p.at_partial = p.at_b + (p.copy_b ? up(rows_b * p.ld_b * size, 16) * 16 : 0);
   p.bytes = p.at_partial + (p.splits > 1 ? p.splits * g.m * partial_ld(g.n) * 4 : 0);
   return p;
+}
+
+ProductKind unsplit_tile(int dtype, const ProductArgs& args) {
+  ProductPlan p;
+  choose_tile(dtype, kPlain, args, 1, p);
+  return p.kind;
+}
+
+int launch_regrid(int dtype, const Regrid& first, const Regrid& second, void* stream, std::string* err) {
+  return prod::regrid(dtype, first, second, reinterpret_cast<hipStream_t>(stream), err);
+}
+
+int launch_join(int dtype, const ProductArgs& args, int splits, void* stream, std::string* err) {
+  return prod::join(dtype, args, splits, reinterpret_cast<hipStream_t>(stream), err);
 }
 
 int launch_product(int dtype, bool a_by_k, bool b_by_k, ProductMode mode, const ProductArgs& args,

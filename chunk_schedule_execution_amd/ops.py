@@ -1,18 +1,20 @@
-"""Products and row exchange beside the collectives, over torch tensors.
+"""Products, row exchange and the layer's operators around them, beside the collectives, over
+torch tensors.
 
-Thin wrappers of the ``ccl_linear*``, ``ccl_grouped_linear*`` and ``ccl_expert_*`` entry
-points: they read shapes, strides and types off the tensors, allocate outputs and
-workspace from torch on the call's stream and launch there (torch's current stream of the
-tensors' device unless ``stream``, a torch stream or a raw handle, is given). A call on
-another stream orders nothing by itself, as with ``Plan.execute``: the caller lets that
-stream wait for the inputs and keeps them (and an ``out`` of its own) until it has passed
-the call. What the call allocates is that stream's, so nothing that torch's current stream
-still works on is written; outputs may be dropped as soon as the current stream's own work
-on them is enqueued. Everything else is in ``libccl.so``. Gradients are explicit calls;
+Thin wrappers of the ``ccl_linear*``, ``ccl_grouped_linear*``, ``ccl_expert_*``,
+``ccl_layer_norm*`` and ``ccl_*cross_entropy*`` entry points: they read shapes, strides and
+types off the tensors, allocate outputs and workspace from torch on the call's stream and launch
+there (torch's current stream of the tensors' device unless ``stream``, a torch stream or a raw
+handle, is given). A call on another stream orders nothing by itself, as with ``Plan.execute``:
+the caller lets that stream wait for the inputs and keeps them (and an ``out`` of its own) until
+it has passed the call. What the call allocates is that stream's, so nothing that torch's
+current stream still works on is written; outputs may be dropped as soon as the current stream's
+own work on them is enqueued. Everything else is in ``libccl.so``. Gradients are explicit calls;
 nothing registers with torch's autograd.
 
-Floating tensors of a call share one type, float32 or bfloat16 (gates are float32).
-Matrices may have rows further apart than their length; their rows must be contiguous.
+Floating tensors of a call share one type, float32 or bfloat16 (gates, the bias that experts are
+ranked with, a norm's statistics and losses are float32). Matrices may have rows further apart
+than their length; their rows must be contiguous.
 """
 
 from __future__ import annotations
@@ -24,6 +26,7 @@ from . import capi
 DTYPES = {torch.float32: capi.CCL_F32, torch.bfloat16: capi.CCL_BF16}
 ACTIVATIONS = {"none": capi.CCL_ACT_NONE, "relu": capi.CCL_ACT_RELU, "gelu": capi.CCL_ACT_GELU,
                "gelu_tanh": capi.CCL_ACT_GELU_TANH, "silu": capi.CCL_ACT_SILU}
+SCORES = {"softmax": capi.CCL_SCORE_SOFTMAX, "sigmoid": capi.CCL_SCORE_SIGMOID}
 
 
 # ---- arguments ----------------------------------------------------------------------
@@ -370,3 +373,219 @@ def expert_combine_backward(dout, h, positions, slots, gates=None, stream=None):
                                          dgates.data_ptr(), handle)
         on.give(dh, dgates)
     return dh, dgates
+
+
+# ---- choice of experts ------------------------------------------------------------------
+def _select_desc(logits, choices, score, groups, kept_groups, group_best, renormalise, scale):
+    if score not in SCORES:
+        _refuse(f"unknown score {score!r}")
+    tokens, experts = logits.shape
+    return capi.ccl_select_desc(DTYPES[logits.dtype], SCORES[score], tokens, experts, choices, groups,
+                                groups if kept_groups is None else kept_groups, group_best, int(bool(renormalise)),
+                                scale, _ld(logits, "logits"))
+
+
+def expert_select(logits, choices, score="softmax", bias=None, groups=1, kept_groups=None, group_best=1,
+                  renormalise=False, scale=1.0, stream=None):
+    """The experts of every token: logits (tokens, experts) -> (ids (tokens, choices) int32,
+    gates (tokens, choices) float32), which ``expert_route`` and ``expert_combine`` take.
+
+    p is the softmax of a token's logits or their sigmoids (``score``). Experts are ranked by
+    p + bias (bias (experts,) float32 or None, compared in 64 bits; ties go to the lower
+    index); with ``kept_groups`` < ``groups`` only within the groups of neighbouring experts
+    whose ``group_best`` (1 or 2) highest values sum up highest. gates: scale p of the chosen
+    experts, divided by the sum of their p with ``renormalise``. An expert whose logit or bias
+    is -inf is never chosen; a token with fewer open ones than ``choices`` gets ids -1 and
+    gates 0 behind them. Autograd does not see the call."""
+    device = _first(logits, "logits")
+    tokens, experts = logits.shape
+    d = _select_desc(logits, choices, score, groups, kept_groups, group_best, renormalise, scale)
+    pb = 0 if bias is None else _packed(bias, "bias", (experts,), torch.float32, device)
+    if not 1 <= choices <= experts:
+        _refuse(f"choices: 1 .. {experts} wanted, not {choices}")
+    on = _on(device, stream)
+    with on as handle:
+        ids = torch.empty(tokens, choices, dtype=torch.int32, device=logits.device)
+        gates = torch.empty(tokens, choices, dtype=torch.float32, device=logits.device)
+        capi.ccl_expert_select(d, logits.data_ptr(), pb, ids.data_ptr(), gates.data_ptr(), handle)
+        on.give(ids, gates)
+    return ids, gates
+
+
+def expert_select_backward(dgates, logits, ids, score="softmax", renormalise=False, scale=1.0, stream=None):
+    """Gradient of ``expert_select``'s gates by the logits, (tokens, experts) of their type:
+    what was chosen counts as fixed, and so do bias and groups."""
+    device = _first(logits, "logits")
+    if not isinstance(ids, torch.Tensor) or ids.dim() != 2:
+        _refuse("ids: (tokens, choices) wanted")
+    tokens, experts = logits.shape
+    pi = _packed(ids, "ids", (tokens, ids.shape[1]), torch.int32, device)
+    pd = _packed(dgates, "dgates", ids.shape, torch.float32, device)
+    d = _select_desc(logits, ids.shape[1], score, 1, 1, 1, renormalise, scale)
+    on = _on(device, stream)
+    with on as handle:
+        dlogits = torch.empty(tokens, experts, dtype=logits.dtype, device=logits.device)
+        capi.ccl_expert_select_backward(d, pd, logits.data_ptr(), pi, dlogits.data_ptr(), handle)
+        on.give(dlogits)
+    return dlogits
+
+
+# ---- layer norm ---------------------------------------------------------------------------
+def layer_norm(x, weight=None, bias=None, residual=None, eps=1e-5, save_stats=False, out=None, total=None,
+               stream=None):
+    """(h - mean) rstd weight + bias with h = x + residual: x and residual (rows, width),
+    weight and bias (width,). Returns out; with a residual also total, h rounded to the type
+    (the norm sees it unrounded); with ``save_stats`` also mean and rstd, (rows,) float32:
+    (out[, total][, mean, rstd]). ``layer_norm_backward`` takes total (x without a residual)
+    and the statistics. Autograd does not see the call."""
+    device = _first(x, "x")
+    rows, width = x.shape
+    dtype = x.dtype
+    pw = 0 if weight is None else _packed(weight, "weight", (width,), dtype, device)
+    pb = 0 if bias is None else _packed(bias, "bias", (width,), dtype, device)
+    pr = ldr = ldo = pt = ldt = 0
+    if residual is not None:
+        _like(residual, "residual", (rows, width), dtype, device)
+        pr, ldr = residual.data_ptr(), _ld(residual, "residual")
+    elif total is not None:
+        _refuse("total: without a residual it is x")
+    ldx = _ld(x, "x")
+    if out is not None:
+        _like(out, "out", (rows, width), dtype, device)
+        ldo = _ld(out, "out")
+    if total is not None:
+        _like(total, "total", (rows, width), dtype, device)
+        ldt = _ld(total, "total")
+    on = _on(device, stream)
+    with on as handle:
+        made_out, made_total = out is None, total is None and residual is not None
+        if made_out:
+            out = torch.empty(rows, width, dtype=dtype, device=x.device)
+        if made_total:
+            total = torch.empty(rows, width, dtype=dtype, device=x.device)
+        if total is not None:
+            pt = total.data_ptr()
+        mean = torch.empty(rows, dtype=torch.float32, device=x.device) if save_stats else None
+        rstd = torch.empty(rows, dtype=torch.float32, device=x.device) if save_stats else None
+        d = capi.ccl_norm_desc(DTYPES[dtype], eps, rows, width, ldx, ldr, ldo, ldt)
+        capi.ccl_layer_norm(d, x.data_ptr(), pr, pw, pb, out.data_ptr(), pt, mean.data_ptr() if save_stats else 0,
+                            rstd.data_ptr() if save_stats else 0, handle)
+        on.give(out if made_out else None, total if made_total else None, mean, rstd)
+    if total is None and not save_stats:
+        return out
+    return (out,) + ((total,) if total is not None else ()) + ((mean, rstd) if save_stats else ())
+
+
+def layer_norm_backward(dout, x, mean, rstd, weight=None, dtotal=None, bias=False, need_dx=True, need_dweight=True,
+                        stream=None):
+    """Gradients of ``layer_norm``: [dx, dweight, dbias], without those that are not needed
+    (dweight belongs to a call with a weight, dbias to ``bias``). x is what was normalised:
+    the forward call's total where it had a residual, whose gradient is dx too. dtotal (rows,
+    width): the gradient that reaches total from elsewhere, added to dx."""
+    device = _first(x, "x")
+    rows, width = x.shape
+    dtype = x.dtype
+    _like(dout, "dout", (rows, width), dtype, device)
+    pm, ps = _packed(mean, "mean", (rows,), torch.float32, device), _packed(rstd, "rstd", (rows,), torch.float32, device)
+    pw = 0 if weight is None else _packed(weight, "weight", (width,), dtype, device)
+    pt = ldt = 0
+    if dtotal is not None:
+        _like(dtotal, "dtotal", (rows, width), dtype, device)
+        pt, ldt = dtotal.data_ptr(), _ld(dtotal, "dtotal")
+    need_dweight = need_dweight and weight is not None
+    d = capi.ccl_norm_desc(DTYPES[dtype], 0.0, rows, width, _ld(x, "x"), 0, _ld(dout, "dout"), 0, ldt)
+    on = _on(device, stream)
+    with on as handle:
+        dx = torch.empty(rows, width, dtype=dtype, device=x.device) if need_dx else None
+        dw = torch.empty(width, dtype=dtype, device=x.device) if need_dweight else None
+        db = torch.empty(width, dtype=dtype, device=x.device) if bias else None
+        nbytes = capi.ccl_layer_norm_backward_workspace(d) if need_dweight or bias else 0
+        ws = _workspace(nbytes, x.device)
+        capi.ccl_layer_norm_backward(d, dout.data_ptr(), x.data_ptr(), pm, ps, pw, pt, dx.data_ptr() if need_dx else 0,
+                                     dw.data_ptr() if need_dweight else 0, db.data_ptr() if bias else 0,
+                                     ws.data_ptr() if nbytes else 0, nbytes, handle)
+        on.give(dx, dw, db)
+    return [t for t in (dx, dw, db) if t is not None]
+
+
+# ---- cross entropy over a vocabulary --------------------------------------------------------
+def _loss_desc(x, w, targets, shard, device):
+    """(descriptor, targets' address)."""
+    if not isinstance(w, torch.Tensor) or w.dim() != 2:
+        _refuse("w: (vocabulary, in) wanted")
+    rows, k = x.shape
+    _like(w, "w", (w.shape[0], k), x.dtype, device)
+    if shard is not None and shard < 0:
+        _refuse("shard: the vocabulary's index of w's first row wanted")
+    pt = _packed(targets, "targets", (rows,), torch.int32, device)
+    d = capi.ccl_cross_entropy_desc(DTYPES[x.dtype], 0, rows, k, w.shape[0], -1 if shard is None else shard,
+                                    _ld(x, "x"), _ld(w, "w"))
+    if (x.data_ptr() | w.data_ptr()) % 16:
+        d.flags = capi.CCL_LINEAR_UNALIGNED
+    return d, pt
+
+
+def linear_cross_entropy(x, w, targets, shard=None, stream=None):
+    """Cross entropy of the logits z = x w^T, which are not kept: x (rows, in), w (vocabulary,
+    in), targets (rows,) int32 -> (loss, lse), (rows,) float32, with lse = log sum exp z and
+    loss = lse - z at the target. A row whose target is negative or past the vocabulary is
+    left out: loss 0, no gradient.
+
+    With ``shard``, w holds the rows of the vocabulary from that index on (one rank's share),
+    and the call returns (lse, picked): lse over them, picked the target's logit, 0 where the
+    target is another shard's. ``cross_entropy_join`` makes loss and lse of all shards' pairs,
+    gathered. Autograd does not see the call."""
+    device = _first(x, "x")
+    d, pt = _loss_desc(x, w, targets, shard, device)
+    on = _on(device, stream)
+    with on as handle:
+        first = torch.empty(x.shape[0], dtype=torch.float32, device=x.device)
+        second = torch.empty(x.shape[0], dtype=torch.float32, device=x.device)
+        nbytes = capi.ccl_linear_cross_entropy_workspace(d, False)
+        ws = _workspace(nbytes, x.device)
+        p1, p2 = first.data_ptr(), second.data_ptr()
+        loss, lse, picked = (p1, p2, 0) if shard is None else (0, p1, p2)
+        capi.ccl_linear_cross_entropy(d, x.data_ptr(), w.data_ptr(), pt, loss, lse, picked,
+                                      ws.data_ptr() if nbytes else 0, nbytes, handle)
+        on.give(first, second)
+    return first, second
+
+
+def cross_entropy_join(lse, picked, targets, stream=None):
+    """(loss, lse) over a whole vocabulary from its shards' lse and picked, (shards, rows)
+    float32 each: what an AllGather of ``linear_cross_entropy``'s results gives."""
+    if not isinstance(lse, torch.Tensor) or lse.dim() != 2:
+        _refuse("lse: (shards, rows) wanted")
+    shards, rows = lse.shape
+    device = lse.get_device()
+    pl, pp = (_packed(t, name, (shards, rows), torch.float32, device) for t, name in ((lse, "lse"), (picked, "picked")))
+    pt = _packed(targets, "targets", (rows,), torch.int32, device)
+    on = _on(device, stream)
+    with on as handle:
+        loss = torch.empty(rows, dtype=torch.float32, device=lse.device)
+        total = torch.empty(rows, dtype=torch.float32, device=lse.device)
+        capi.ccl_cross_entropy_join(shards, rows, pl, pp, pt, loss.data_ptr(), total.data_ptr(), handle)
+        on.give(loss, total)
+    return loss, total
+
+
+def linear_cross_entropy_backward(dloss, x, w, targets, lse, shard=None, need_dx=True, need_dw=True, stream=None):
+    """Gradients of the loss: [dx, dw], without those that are not needed. dloss (rows,)
+    float32; lse is the whole vocabulary's. The logits are computed again, in pieces of the
+    vocabulary. With ``shard`` dx is this shard's summand (an AllReduce adds them up), dw its
+    own. dz is rounded to the tensors' type for the two products, as ``linear_backward``'s is."""
+    device = _first(x, "x")
+    d, pt = _loss_desc(x, w, targets, shard, device)
+    rows = x.shape[0]
+    pd, pl = _packed(dloss, "dloss", (rows,), torch.float32, device), _packed(lse, "lse", (rows,), torch.float32, device)
+    on = _on(device, stream)
+    with on as handle:
+        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if need_dx else None
+        dw = torch.empty(w.shape, dtype=x.dtype, device=x.device) if need_dw else None
+        nbytes = capi.ccl_linear_cross_entropy_workspace(d, True)
+        ws = _workspace(nbytes, x.device)
+        capi.ccl_linear_cross_entropy_backward(d, pd, x.data_ptr(), w.data_ptr(), pt, pl, dx.data_ptr() if need_dx else 0,
+                                               dw.data_ptr() if need_dw else 0, ws.data_ptr() if nbytes else 0, nbytes,
+                                               handle)
+        on.give(dx, dw)
+    return [t for t in (dx, dw) if t is not None]

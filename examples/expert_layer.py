@@ -1,11 +1,11 @@
 """An expert-parallel layer on virtual ranks: the collectives and the products together.
 
-Every rank holds its own tokens and a share of the experts. Per rank: router scores
-(``ops.linear``), a route of the tokens' choices by expert (``ops.expert_route``,
-``ops.expert_dispatch``), an AllToAll that takes rows to their experts' ranks (``Plan``),
-the experts' two products (``ops.grouped_linear``), an AllToAll back, the gated sum
-(``ops.expert_combine``) and a tensor-parallel output projection whose partial products an
-AllReduce sums. Run it on an MI355X:
+Every rank holds its own tokens and a share of the experts. Per rank: router logits
+(``ops.linear``), the choice of experts (``ops.expert_select``), a route of the tokens'
+choices by expert (``ops.expert_route``, ``ops.expert_dispatch``), an AllToAll that takes
+rows to their experts' ranks (``Plan``), the experts' two products (``ops.grouped_linear``),
+an AllToAll back, the gated sum (``ops.expert_combine``) and a tensor-parallel output
+projection whose partial products an AllReduce sums. Run it on an MI355X:
 
     python examples/expert_layer.py
 """
@@ -57,9 +57,7 @@ class ExpertLayer:
         P, C, W, L = self.ranks, self.block, self.width, self.local
         routes, sent, counts = [], [], []
         for x in xs:
-            scores = ops.linear(x, self.router).float()
-            top = scores.topk(self.choices, dim=1)
-            ids, gates = top.indices.to(torch.int32), torch.softmax(top.values, dim=1)
+            ids, gates = ops.expert_select(ops.linear(x, self.router), self.choices, renormalise=True)
             offsets, positions, slots = ops.expert_route(ids, self.experts)
             rows = ops.expert_dispatch(x, slots, self.choices)
             # rank d's rows follow each other; row i goes to place i - begin of block d

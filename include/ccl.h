@@ -667,6 +667,124 @@ int ccl_expert_combine_backward(int dtype, const void* dout, int64_t ld_dout, co
                                 const int32_t* positions, const int32_t* slots, const float* gates, int64_t tokens,
                                 int choices, int64_t width, void* dh, int64_t ld_dh, float* dgates, void* stream);
 
+/* ---- the layer's operators around the products ------------------------------
+ *
+ * What a rank computes around the products and the row exchange in a step of a model whose
+ * experts and vocabulary are spread over ranks: the choice of experts before the exchange,
+ * layer norm between an AllReduce and the next product, and the loss over a vocabulary or
+ * over the rank's shard of it. The common rules above hold.
+ */
+#define CCL_SCORE_SOFTMAX 0
+#define CCL_SCORE_SIGMOID 1
+
+typedef struct {
+  int32_t dtype;       /* of the logits and their gradients: CCL_F32 or CCL_BF16 */
+  int32_t score;       /* CCL_SCORE_* */
+  int64_t tokens;      /* 0 .. 2^31 - 1 */
+  int32_t experts;     /* 1 .. 1024 */
+  int32_t choices;     /* 1 .. 64, at most `experts` */
+  int32_t groups;      /* 1 .. 64 groups of experts / groups neighbouring experts (it divides) */
+  int32_t kept_groups; /* 1 .. groups: those that experts are chosen from */
+  int32_t group_best;  /* 1 or 2: how many of a group's highest values make the group's */
+  int32_t renormalise; /* 1: a token's gates are divided by their sum */
+  float scale;         /* finite: multiplies the gates */
+  int64_t ld_logits, ld_dlogits;
+} ccl_select_desc;
+
+/*
+ * The choice of experts. p = softmax of a token's logits over all experts, or their sigmoids.
+ * Experts are ranked by p + bias (bias: fp32 by expert, or NULL), compared in 64 bits; without
+ * a bias by their logits, which is the same order. With kept_groups < groups, only the experts
+ * of the kept_groups groups of highest value stay, a group's value being the sum of the
+ * group_best highest values p + bias of its experts. The `choices` highest of what stays are
+ * chosen, in descending order; ties go to the lower index. gates = scale p of the chosen ones,
+ * divided by the sum of their p with renormalise; the bias is no part of a gate.
+ * An expert whose logit or bias is -inf is closed: it is never chosen and adds nothing to a
+ * group. Where fewer than `choices` are open, the rest of the token's ids are -1 (which
+ * ccl_expert_route reads as no row) and their gates 0. A NaN ranks as +inf; the gates that
+ * depend on it are NaN. ids, gates: tokens x choices.
+ * Errors: INVALID_ARGUMENT, UNSUPPORTED (dtype, score), HIP.
+ */
+int ccl_expert_select(const ccl_select_desc* desc, const void* logits, const float* bias, int32_t* ids, float* gates,
+                      void* stream);
+
+/* Gradient of the gates by the logits, tokens x experts: what is chosen counts as fixed. With
+ * softmax and without renormalise every open expert has one; otherwise only the chosen ones.
+ * ids: the choice's; a choice whose id is not an expert's has no part. groups, kept_groups and
+ * group_best are not used but checked. */
+int ccl_expert_select_backward(const ccl_select_desc* desc, const float* dgates, const void* logits,
+                               const int32_t* ids, void* dlogits, void* stream);
+
+typedef struct {
+  int32_t dtype;  /* CCL_F32 or CCL_BF16: every matrix, weight and bias and their gradients */
+  float eps;      /* finite, at least 0 */
+  int64_t rows;   /* 0 .. 2^31 - 1 */
+  int64_t width;  /* 1 .. 2^20 */
+  int64_t ld_x, ld_residual, ld_out, ld_total, ld_dtotal, ld_dx; /* ld_out is also dout's */
+} ccl_norm_desc;
+
+/*
+ * out = (h - mean) rstd weight + bias with h = x + residual, mean and rstd = (variance +
+ * eps)^-1/2 over a row's `width` values, in fp32 (the variance from differences to the mean).
+ * residual, weight and bias may be NULL. total (NULL, or with a residual): receives h, rounded
+ * to the dtype; the norm sees it unrounded. mean, rstd (both or neither): fp32 by row.
+ * Errors: INVALID_ARGUMENT, UNSUPPORTED, HIP.
+ */
+int ccl_layer_norm(const ccl_norm_desc* desc, const void* x, const void* residual, const void* weight,
+                   const void* bias, void* out, void* total, float* mean, float* rstd, void* stream);
+
+/*
+ * Gradients. x is what was normalised (total, with a residual), mean and rstd the forward
+ * pass's. With y = (x - mean) rstd and g = dout weight: dx = rstd (g - mean(g) - y mean(g y)) +
+ * dtotal, dweight = column sums of dout y, dbias of dout. dx is also the residual's gradient;
+ * dtotal (or NULL) is the gradient that reaches h past the norm. Any of dx, dweight, dbias may
+ * be NULL; the workspace is needed for the latter two. With rows = 0 those are set to zero.
+ */
+int64_t ccl_layer_norm_backward_workspace(const ccl_norm_desc* desc);
+int ccl_layer_norm_backward(const ccl_norm_desc* desc, const void* dout, const void* x, const float* mean,
+                            const float* rstd, const void* weight, const void* dtotal, void* dx, void* dweight,
+                            void* dbias, void* workspace, size_t workspace_bytes, void* stream);
+
+typedef struct {
+  int32_t dtype;       /* CCL_F32 or CCL_BF16 */
+  uint32_t flags;      /* CCL_LINEAR_UNALIGNED */
+  int64_t rows;        /* 0 .. 2^31 - 1 */
+  int64_t in_features; /* 1 .. 2^20 */
+  int64_t vocabulary;  /* rows of w: 1 .. 2^20 */
+  int64_t first;       /* -1: w is the whole vocabulary; otherwise w is a shard of it and this is
+                          the vocabulary's index of its first row; first + vocabulary < 2^31 */
+  int64_t ld_x, ld_w, ld_dx, ld_dw;
+} ccl_cross_entropy_desc;
+
+/*
+ * Cross entropy of z = x w^T against targets (int32 by row) without keeping z: lse = log sum
+ * exp z over w's rows, picked = z at the target, loss = lse - picked, all fp32 by row. loss and
+ * picked may be NULL. A row whose target is negative is left out: its loss is 0 and it has no
+ * part in a gradient; of a whole vocabulary, so is a target past its end. With a shard, picked
+ * is 0 for a target that is no row of it, and loss has to be NULL: ccl_cross_entropy_join gives
+ * it from all shards' lse and picked.
+ */
+int64_t ccl_linear_cross_entropy_workspace(const ccl_cross_entropy_desc* desc, int backward);
+int ccl_linear_cross_entropy(const ccl_cross_entropy_desc* desc, const void* x, const void* w, const int32_t* targets,
+                             float* loss, float* lse, float* picked, void* workspace, size_t workspace_bytes,
+                             void* stream);
+
+/* lse = log sum exp of the shards' lse_parts (shards x rows), loss = lse - the sum of their
+ * picked_parts, 0 for a negative target. What an AllGather of the shards' sums is joined by. */
+int ccl_cross_entropy_join(int shards, int64_t rows, const float* lse_parts, const float* picked_parts,
+                           const int32_t* targets, float* loss, float* lse, void* stream);
+
+/*
+ * Gradients: dz = dloss (exp(z - lse) - [column is the target]), dx = dz w, dw = dz^T x. lse is
+ * the whole vocabulary's (a shard's call gets the joined one; its dx is the shard's summand,
+ * its dw its own). z is computed again, a piece of the vocabulary at a time: the workspace holds
+ * dz of a piece, 512 MiB or 8192 columns of it. dz is rounded to the dtype for the two products,
+ * as a stored gradient is; sums over pieces are fp32. dx or dw may be NULL.
+ */
+int ccl_linear_cross_entropy_backward(const ccl_cross_entropy_desc* desc, const float* dloss, const void* x,
+                                      const void* w, const int32_t* targets, const float* lse, void* dx, void* dw,
+                                      void* workspace, size_t workspace_bytes, void* stream);
+
 /* ---- errors --------------------------------------------------------------- */
 const char* ccl_error_string(int status);
 const char* ccl_last_error_detail(void);
