@@ -9,7 +9,7 @@ namespace prod {
 // Lane l's value of the lane n further on within the 16 of a row, around its end.
 template <int N>
 __device__ inline int turned(int v) {
-  return __builtin_amdgcn_update_dpp(v, v, 0x120 + N, 0xf, 0xf, false);
+  return __builtin_amdgcn_update_dpp(0, v, 0x120 + N, 0xf, 0xf, true);  // every lane has a source
 }
 template <int N>
 __device__ inline float turned(float v) {
@@ -33,8 +33,11 @@ __device__ inline V over(V v, F f) {
   return v;
 }
 template <int L, typename V>
-__device__ inline V over_max(V v) {
-  return over<L>(v, [](V a, V b) { return a > b ? a : b; });
+__device__ inline V over_max(V v) {  // not of NaN
+  return over<L>(v, [](V a, V b) {
+    if constexpr (sizeof(V) == 4) return __builtin_fmaxf(a, b);
+    else return a > b ? a : b;
+  });
 }
 template <int L, typename V>
 __device__ inline V over_sum(V v) {

@@ -38,6 +38,9 @@ SelectArgs select_args(const ccl_select_desc* d) {
   a.groups = d->groups;
   a.kept = d->kept_groups;
   a.best = d->group_best;
+  a.per = d->experts / d->groups;
+  a.magic = (1 << 20) / a.per + 1;
+  while ((a.groups << (a.parts_log2 + 1)) <= 16) ++a.parts_log2;
   a.score = d->score;
   a.renorm = d->renormalise != 0;
   a.scale = d->scale;
@@ -65,7 +68,7 @@ NormArgs norm_args(const ccl_norm_desc* d) {
   a.ld_dx = stride_of(d->ld_dx, d->width, "ld_dx");
   return a;
 }
-int64_t norm_workspace(const NormArgs& a) { return align16(norm_partials(a.rows, a.width) * 2 * a.width * 4); }
+int64_t norm_workspace(const NormArgs& a) { return align16(norm_partials(a.rows) * 2 * a.width * 4); }
 
 // ---- cross entropy ---------------------------------------------------------------------------
 ccl_cross_entropy_desc checked(const ccl_cross_entropy_desc* d) {

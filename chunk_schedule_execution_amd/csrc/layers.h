@@ -21,6 +21,9 @@ struct SelectArgs {
   int experts = 0, choices = 0, groups = 1, kept = 1, best = 1, score = 0;
   bool renorm = false;
   float scale = 1.0f;
+  // of the groups: experts in each, 2^20 / that + 1, and the lanes of 16 that share one as a
+  // power of 2
+  int per = 0, magic = 0, parts_log2 = 0;
 };
 int launch_select(int dtype, const SelectArgs& args, void* stream, std::string* err);
 int launch_select_backward(int dtype, const SelectArgs& args, void* stream, std::string* err);
@@ -47,7 +50,7 @@ struct NormArgs {
 };
 int launch_norm(int dtype, const NormArgs& args, void* stream, std::string* err);
 // Rows of partial sums that the gradients leave, at most.
-int64_t norm_partials(int64_t rows, int64_t width);
+int64_t norm_partials(int64_t rows);
 int launch_norm_backward(int dtype, const NormArgs& args, void* stream, std::string* err);
 
 // The cross entropy of z = x w^T. A row's target is column target - first of z; it is none

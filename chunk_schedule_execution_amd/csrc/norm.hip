@@ -1,6 +1,8 @@
 // Layer norm with the residual's addition for gfx950, and its gradients. Memory bounds both:
-// a row is read once and stays in registers for its mean, its variance and its result.
+// a row is read once and stays in registers for its mean, its variance and its result, and
+// workgroups walk rows, so that the next row's loads run beside this one's sums.
 #include <algorithm>
+#include <type_traits>
 
 #include "lanes.h"
 #include "layers.h"
@@ -10,31 +12,43 @@ namespace ccl {
 namespace prod {
 namespace {
 
-// V elements as they move: 16 bytes, or one element where rows are off that grid.
-template <typename T, int V>
-struct __attribute__((aligned(sizeof(T) * V))) Pack {
-  T v[V];
-};
+// 16 bytes of a row wherever they lie: loads and stores of vectors need no alignment beyond
+// the element's, and a row's last vector may be cut short (`left` values to its end). Rows are
+// read and written once: around the caches.
+template <typename T>
+struct Pack {
+  static constexpr int kValues = 16 / int(sizeof(T));
+  typedef T vec __attribute__((ext_vector_type(kValues), aligned(sizeof(T))));
+  vec v;
 
-// Rows are read and written once: around the caches.
-template <typename T, int V>
-__device__ inline Pack<T, V> load_once(const Pack<T, V>* from) {
-  if constexpr (sizeof(Pack<T, V>) == 16) {
+  __device__ inline void zero() { v = vec(T(0.0f)); }
+  // The same values, from which nothing is kept that was computed before.
+  __device__ inline void renew() {
     typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
-    return __builtin_bit_cast(Pack<T, V>, __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(from)));
-  } else {
-    return *from;
+    u32x4 bits = __builtin_bit_cast(u32x4, v);
+    asm volatile("" : "+v"(bits));
+    v = __builtin_bit_cast(vec, bits);
   }
-}
-template <typename T, int V>
-__device__ inline void store_once(Pack<T, V>* to, const Pack<T, V>& x) {
-  if constexpr (sizeof(x) == 16) {
-    typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
-    __builtin_nontemporal_store(__builtin_bit_cast(u32x4, x), reinterpret_cast<u32x4*>(to));
-  } else {
-    *to = x;
+  template <bool Once = true>
+  __device__ inline void load(const T* p, int left) {
+    if (left >= kValues) {
+      if constexpr (Once) v = __builtin_nontemporal_load(reinterpret_cast<const vec*>(p));
+      else v = *reinterpret_cast<const vec*>(p);
+    } else {
+#pragma unroll
+      for (int q = 0; q < kValues; ++q) v[q] = q < left ? p[q] : T(0.0f);
+    }
   }
-}
+  __device__ inline void store(T* p, int left) const {
+    if (left >= kValues) {
+      __builtin_nontemporal_store(v, reinterpret_cast<vec*>(p));
+    } else {
+#pragma unroll
+      for (int q = 0; q < kValues; ++q)
+        if (q < left) p[q] = v[q];
+    }
+  }
+};
 
 // All waves' LDS accesses before this point are done; loads from memory stay in flight.
 __device__ inline void lds_barrier() {
@@ -50,102 +64,132 @@ inline dim3 flat_grid(int64_t n) {
   return dim3(unsigned(x), unsigned((n + x - 1) / x));
 }
 
-// ---- forward -------------------------------------------------------------------------------
-// The sum of v over the R threads of a row: a wave, or the workgroup's four.
+// How the threads share out rows of packs: R threads to a row, `Held` packs each, and as many
+// rows side by side as a workgroup of 256 holds. One wave to a row needs no barrier.
+template <int R>
+struct Sharing {
+  static constexpr int kThreads = R < 256 ? 256 : R, kRows = kThreads / R, kWaves = R / 64;
+};
+
+// The sum of v over the R threads of a row. parts: LDS that is not used again before the
+// workgroup's next barrier but one.
 template <int R>
 __device__ inline float row_sum(float v, float* parts) {
   v = over_sum<64>(v);
-  if constexpr (R == 64) {
-    return v;
-  } else {
+  if constexpr (R > 64) {
     if (threadIdx.x % 64 == 0) parts[threadIdx.x / 64] = v;
     lds_barrier();
-    return (parts[0] + parts[1]) + (parts[2] + parts[3]);
+    v = 0.0f;
+#pragma unroll
+    for (int i = 0; i < R / 64; ++i) v += parts[i];
+  }
+  return v;
+}
+
+// Of two values with one barrier.
+template <int R>
+__device__ inline void row_sums(float& v, float& w, float (*parts)[Sharing<R>::kWaves]) {
+  v = over_sum<64>(v);
+  w = over_sum<64>(w);
+  if constexpr (R > 64) {
+    if (threadIdx.x % 64 == 0) {
+      parts[0][threadIdx.x / 64] = v;
+      parts[1][threadIdx.x / 64] = w;
+    }
+    lds_barrier();
+    v = w = 0.0f;
+#pragma unroll
+    for (int i = 0; i < R / 64; ++i) {
+      v += parts[0][i];
+      w += parts[1][i];
+    }
   }
 }
 
-// R threads hold a row, Held packs each. The variance is the mean of squared differences
-// from the mean, from registers: nothing cancels.
-template <typename T, int V, int Held, int R>
-__global__ __launch_bounds__(256) void norm_kernel(NormArgs a) {
-  using P = Pack<T, V>;
-  __shared__ float parts[2][4];
-  const int lane = threadIdx.x % R;
-  const int64_t row = flat_block() * (256 / R) + threadIdx.x / R;
-  if (row >= a.rows) return;  // a whole wave, or the workgroup
-  const int n = int(a.width / V);
-  const P* x = reinterpret_cast<const P*>(static_cast<const T*>(a.x) + row * a.ld_x);
-  float h[Held][V];
-  float sum = 0.0f;
-  if (a.residual) {
-    const P* r = reinterpret_cast<const P*>(static_cast<const T*>(a.residual) + row * a.ld_residual);
-    P px[Held], pr[Held];
+// ---- forward -------------------------------------------------------------------------------
+// The variance is the mean of squared differences from the mean, from registers: nothing
+// cancels. 16384 x 4096 bf16 with residual and both outputs (537 MB): 106 us with one row per
+// wave and no walk.
+template <typename T, int Held, int R>
+__global__ __launch_bounds__(Sharing<R>::kThreads) void norm_kernel(NormArgs a) {
+  using P = Pack<T>;
+  constexpr int V = P::kValues, Rows = Sharing<R>::kRows;
+  __shared__ float parts[2][2][Sharing<R>::kWaves];
+  const int lane = threadIdx.x % R, width = int(a.width);
+  P pw[Held], pb[Held], px[Held], pr[Held];
 #pragma unroll
-    for (int i = 0; i < Held; ++i)
-      if (i * R + lane < n) {
-        px[i] = load_once(x + i * R + lane);
-        pr[i] = load_once(r + i * R + lane);
-      }
-    P* total = reinterpret_cast<P*>(static_cast<T*>(a.total) + row * a.ld_total);
+  for (int i = 0; i < Held; ++i) {
+    const int c = (i * R + lane) * V;
+    pw[i].zero();
+    pb[i].zero();
+    px[i].zero();
+    pr[i].zero();
+    if (a.weight) pw[i].template load<false>(static_cast<const T*>(a.weight) + c, width - c);
+    if (a.bias) pb[i].template load<false>(static_cast<const T*>(a.bias) + c, width - c);
+  }
+  auto load = [&](int64_t row) {
+    const T* x = static_cast<const T*>(a.x) + row * a.ld_x;
+    const T* r = static_cast<const T*>(a.residual) + row * a.ld_residual;
 #pragma unroll
     for (int i = 0; i < Held; ++i) {
-      const bool in = i * R + lane < n;
+      const int c = (i * R + lane) * V;
+      px[i].load(x + c, width - c);
+      if (a.residual) pr[i].load(r + c, width - c);
+    }
+  };
+  const int64_t step = int64_t(gridDim.x) * Rows;
+  int64_t row = int64_t(blockIdx.x) * Rows + threadIdx.x / R;
+  int turn = 0;
+  if (row < a.rows) load(row);
+  for (; row < a.rows; row += step, turn ^= 1) {
+    float h[Held][V], sum = 0.0f, squares = 0.0f;
 #pragma unroll
-      for (int q = 0; q < V; ++q) h[i][q] = in ? widen(px[i].v[q]) + widen(pr[i].v[q]) : 0.0f;
-      if (in && a.total) {
+    for (int i = 0; i < Held; ++i)
+#pragma unroll
+      for (int q = 0; q < V; ++q) {
+        h[i][q] = widen(px[i].v[q]);
+        if (a.residual) h[i][q] += widen(pr[i].v[q]);
+        sum += h[i][q];
+      }
+    if (row + step < a.rows) load(row + step);
+    if (a.total) {
+      T* total = static_cast<T*>(a.total) + row * a.ld_total;
+#pragma unroll
+      for (int i = 0; i < Held; ++i) {
+        const int c = (i * R + lane) * V;
         P o;
 #pragma unroll
         for (int q = 0; q < V; ++q) o.v[q] = narrow<T>(h[i][q]);
-        store_once(total + i * R + lane, o);
+        o.store(total + c, width - c);
       }
     }
-  } else {
-    P px[Held];
+    const float mean = row_sum<R>(sum, parts[turn][0]) / float(width);
 #pragma unroll
     for (int i = 0; i < Held; ++i)
-      if (i * R + lane < n) px[i] = load_once(x + i * R + lane);
-#pragma unroll
-    for (int i = 0; i < Held; ++i)
-#pragma unroll
-      for (int q = 0; q < V; ++q) h[i][q] = i * R + lane < n ? widen(px[i].v[q]) : 0.0f;
-  }
-#pragma unroll
-  for (int i = 0; i < Held; ++i)
-#pragma unroll
-    for (int q = 0; q < V; ++q) sum += h[i][q];
-  const float mean = row_sum<R>(sum, parts[0]) / float(a.width);
-  float squares = 0.0f;
-#pragma unroll
-  for (int i = 0; i < Held; ++i)
-    if (i * R + lane < n)
 #pragma unroll
       for (int q = 0; q < V; ++q) {
         h[i][q] -= mean;
-        squares = fmaf(h[i][q], h[i][q], squares);
+        squares += (i * R + lane) * V + q < width ? h[i][q] * h[i][q] : 0.0f;
       }
-  const float rstd = 1.0f / sqrtf(row_sum<R>(squares, parts[1]) / float(a.width) + a.eps);
-  if (a.mean && lane == 0) {
-    a.mean[row] = mean;
-    a.rstd[row] = rstd;
-  }
-  const P* w = static_cast<const P*>(a.weight);
-  const P* b = static_cast<const P*>(a.bias);
-  P* out = reinterpret_cast<P*>(static_cast<T*>(a.out) + row * a.ld_out);
-#pragma unroll
-  for (int i = 0; i < Held; ++i) {
-    const int c = i * R + lane;
-    if (c >= n) continue;
-    P o, pw, pb;
-    if (w) pw = w[c];
-    if (b) pb = b[c];
-#pragma unroll
-    for (int q = 0; q < V; ++q) {
-      float v = h[i][q] * rstd;
-      if (w) v *= widen(pw.v[q]);
-      if (b) v += widen(pb.v[q]);
-      o.v[q] = narrow<T>(v);
+    const float rstd = 1.0f / sqrtf(row_sum<R>(squares, parts[turn][1]) / float(width) + a.eps);
+    if (a.mean && lane == 0) {
+      a.mean[row] = mean;
+      a.rstd[row] = rstd;
     }
-    store_once(out + c, o);
+    T* out = static_cast<T*>(a.out) + row * a.ld_out;
+#pragma unroll
+    for (int i = 0; i < Held; ++i) {
+      const int c = (i * R + lane) * V;
+      P o;
+#pragma unroll
+      for (int q = 0; q < V; ++q) {
+        float v = h[i][q] * rstd;
+        if (a.weight) v *= widen(pw[i].v[q]);
+        if (a.bias) v += widen(pb[i].v[q]);
+        o.v[q] = narrow<T>(v);
+      }
+      o.store(out + c, width - c);
+    }
   }
 }
 
@@ -225,100 +269,133 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(NormArgs a) {
 
 // ---- gradients -----------------------------------------------------------------------------
 // With g = dout w and y = (x - mean) rstd: dx = rstd (g - mean(g) - y mean(g y)) + dtotal,
-// dw = sum over the rows of dout y, db of dout. A workgroup walks rows, Held packs of a row
-// per thread, always the same columns, whose share of dw and db stays in registers: one pass
-// over the rows gives all three. Each workgroup leaves its share in `partial`.
-template <typename T, int V, int Held, int Threads>
-__global__ __launch_bounds__(Threads) void norm_backward_kernel(NormArgs a) {
-  using P = Pack<T, V>;
-  constexpr int Waves = Threads / 64;
-  __shared__ float parts[2][Waves][2];
-  const int tid = threadIdx.x, n = int(a.width / V);
-  float dw[Held][V] = {}, db[Held][V] = {}, w[Held][V];
+// dw = sum over the rows of dout y, db of dout. A thread keeps to its columns, whose share of dw
+// and db stays in registers: one pass over the rows gives all three, and each workgroup leaves
+// its share in `partial`. 16384 x 4096 bf16 with dtotal (537 MB): 94 us, 5.7 TB/s; 134 without
+// the next row's loads ahead.
+template <typename T, int Held, int R>
+__global__ __launch_bounds__(Sharing<R>::kThreads) void norm_backward_kernel(NormArgs a) {
+  using P = Pack<T>;
+  constexpr int V = P::kValues, Rows = Sharing<R>::kRows;
+  constexpr bool Ahead = Held * V < 32;  // more values of three tensors twice do not fit the registers
+  __shared__ float parts[2][2][Sharing<R>::kWaves];
+  const int lane = threadIdx.x % R, width = int(a.width);
+  float dw[Held][V] = {}, db[Held][V] = {};
+  P pw[Held], px[Held], pd[Held], pt[Held];
 #pragma unroll
-  for (int i = 0; i < Held; ++i)
-#pragma unroll
-    for (int q = 0; q < V; ++q)
-      w[i][q] = a.weight && i * Threads + tid < n ? widen(static_cast<const P*>(a.weight)[i * Threads + tid].v[q]) : 1.0f;
-  P px[Held], pd[Held], pt[Held];
+  for (int i = 0; i < Held; ++i) {
+    const int c = (i * R + lane) * V;
+    pw[i].zero();
+    px[i].zero();
+    pd[i].zero();
+    pt[i].zero();
+    if (a.weight) pw[i].template load<false>(static_cast<const T*>(a.weight) + c, width - c);
+  }
   float mean = 0.0f, rstd = 0.0f;
   auto load = [&](int64_t row) {
-    const P* x = reinterpret_cast<const P*>(static_cast<const T*>(a.x) + row * a.ld_x);
-    const P* d = reinterpret_cast<const P*>(static_cast<const T*>(a.dout) + row * a.ld_out);
+    const T* x = static_cast<const T*>(a.x) + row * a.ld_x;
+    const T* d = static_cast<const T*>(a.dout) + row * a.ld_out;
+    const T* t = static_cast<const T*>(a.dtotal) + row * a.ld_dtotal;
     mean = a.mean[row];
     rstd = a.rstd[row];
 #pragma unroll
-    for (int i = 0; i < Held; ++i)
-      if (i * Threads + tid < n) {
-        px[i] = load_once(x + i * Threads + tid);
-        pd[i] = load_once(d + i * Threads + tid);
-      }
-    if (a.dtotal) {
-      const P* t = reinterpret_cast<const P*>(static_cast<const T*>(a.dtotal) + row * a.ld_dtotal);
-#pragma unroll
-      for (int i = 0; i < Held; ++i)
-        if (i * Threads + tid < n) pt[i] = load_once(t + i * Threads + tid);
+    for (int i = 0; i < Held; ++i) {
+      const int c = (i * R + lane) * V;
+      px[i].load(x + c, width - c);
+      pd[i].load(d + c, width - c);
+      if (a.dtotal) pt[i].load(t + c, width - c);
     }
   };
+  const int64_t step = int64_t(gridDim.x) * Rows;
+  int64_t row = int64_t(blockIdx.x) * Rows + threadIdx.x / R;
   int turn = 0;
-  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
-    load(row);
-    float y[Held][V], g[Held][V], sum = 0.0f, dot = 0.0f;
+  if (Ahead && row < a.rows) load(row);
+  for (; row < a.rows; row += step, turn ^= 1) {
+    if (!Ahead) load(row);
+    P cx[Held], cd[Held], ct[Held];
+#pragma unroll
+    for (int i = 0; i < Held; ++i) {
+      cx[i] = px[i];
+      cd[i] = pd[i];
+      ct[i] = pt[i];
+    }
+    const float m = mean, r = rstd;
+    if (Ahead && row + step < a.rows) load(row + step);
+    // dout is 0 past the row's end, so nothing there reaches a sum
+    float sum = 0.0f, dot = 0.0f;
 #pragma unroll
     for (int i = 0; i < Held; ++i)
 #pragma unroll
       for (int q = 0; q < V; ++q) {
-        const bool in = i * Threads + tid < n;
-        const float d = in ? widen(pd[i].v[q]) : 0.0f;
-        y[i][q] = in ? (widen(px[i].v[q]) - mean) * rstd : 0.0f;
-        dw[i][q] = fmaf(d, y[i][q], dw[i][q]);
+        const float d = widen(cd[i].v[q]), y = (widen(cx[i].v[q]) - m) * r;
+        dw[i][q] = fmaf(d, y, dw[i][q]);
         db[i][q] += d;
-        g[i][q] = d * w[i][q];
-        sum += g[i][q];
-        dot = fmaf(g[i][q], y[i][q], dot);
+        const float g = a.weight ? d * widen(pw[i].v[q]) : d;
+        sum += g;
+        dot = fmaf(g, y, dot);
       }
     if (!a.dx) continue;  // the same for all
-    sum = over_sum<64>(sum);
-    dot = over_sum<64>(dot);
-    if (tid % 64 == 0) {
-      parts[turn][tid / 64][0] = sum;
-      parts[turn][tid / 64][1] = dot;
-    }
-    // one barrier a row: the other half of `parts` may still be read
-    lds_barrier();
-    sum = dot = 0.0f;
-#pragma unroll
-    for (int k = 0; k < Waves; ++k) {
-      sum += parts[turn][k][0];
-      dot += parts[turn][k][1];
-    }
-    sum /= float(a.width);
-    dot /= float(a.width);
-    P* dx = reinterpret_cast<P*>(static_cast<T*>(a.dx) + row * a.ld_dx);
+    row_sums<R>(sum, dot, parts[turn]);
+    sum /= float(width);
+    dot /= float(width);
+    T* dx = static_cast<T*>(a.dx) + row * a.ld_dx;
 #pragma unroll
     for (int i = 0; i < Held; ++i) {
-      if (i * Threads + tid >= n) continue;
+      const int c = (i * R + lane) * V;
+      if (Held * V >= 16) {  // y and g again rather than in registers, which they would overflow
+        cx[i].renew();
+        cd[i].renew();
+      }
       P o;
 #pragma unroll
       for (int q = 0; q < V; ++q) {
-        float v = rstd * (g[i][q] - sum - y[i][q] * dot);
-        if (a.dtotal) v += widen(pt[i].v[q]);
+        const float d = widen(cd[i].v[q]), y = (widen(cx[i].v[q]) - m) * r;
+        const float g = a.weight ? d * widen(pw[i].v[q]) : d;
+        float v = r * (g - sum - y * dot);
+        if (a.dtotal) v += widen(ct[i].v[q]);
         o.v[q] = narrow<T>(v);
       }
-      store_once(dx + i * Threads + tid, o);
+      o.store(dx + c, width - c);
     }
   }
   if (!a.partial) return;
-  float* to = a.partial + int64_t(blockIdx.x) * 2 * a.width;
+  float* to = a.partial + int64_t(blockIdx.x) * 2 * width;
+  if constexpr (Rows > 1) {  // the rows side by side, in order
+    __shared__ float sums[2][Rows - 1][Held * R * V];
+    const int mine = threadIdx.x / R;
+#pragma unroll
+    for (int i = 0; i < Held; ++i)
+#pragma unroll
+      for (int q = 0; q < V; ++q)
+        if (mine) {
+          sums[0][mine - 1][(i * V + q) * R + lane] = dw[i][q];
+          sums[1][mine - 1][(i * V + q) * R + lane] = db[i][q];
+        }
+    __syncthreads();
+    if (mine) return;
+    for (int k = 0; k < Rows - 1; ++k)
+#pragma unroll
+      for (int i = 0; i < Held; ++i)
+#pragma unroll
+        for (int q = 0; q < V; ++q) {
+          dw[i][q] += sums[0][k][(i * V + q) * R + lane];
+          db[i][q] += sums[1][k][(i * V + q) * R + lane];
+        }
+  }
 #pragma unroll
   for (int i = 0; i < Held; ++i)
-    if (i * Threads + tid < n)
 #pragma unroll
-      for (int q = 0; q < V; ++q) {
-        const int64_t c = int64_t(i * Threads + tid) * V + q;
-        to[c] = dw[i][q];
-        to[a.width + c] = db[i][q];
+    for (int q = 0; q < V; q += 4) {
+      const int c = (i * R + lane) * V + q;
+      Pack<float> w, b;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        w.v[j] = dw[i][q + j];
+        b.v[j] = db[i][q + j];
       }
+      w.store(to + c, width - c);
+      b.store(to + width + c, width - c);
+    }
 }
 
 // Rows that registers do not hold. dx: a workgroup a row, read twice.
@@ -432,85 +509,72 @@ __global__ __launch_bounds__(1024) void norm_sum_kernel(NormArgs a, int64_t shar
 }
 
 // ---- choice of kernels -----------------------------------------------------------------------
-template <typename T>
-bool on_grid(const void* p, int64_t ld) {
-  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * sizeof(T) % 16 == 0;
+// Calls f with the threads to a row and the packs of each that hold a row of n packs; false
+// where none do. Eight only in fp32, where they are as many values as four in bf16.
+template <typename T, typename F>
+bool by_width(int64_t n, F f) {
+  using std::integral_constant;
+  const integral_constant<int, 1> one;
+  const integral_constant<int, 2> two;
+  const integral_constant<int, 512> most;
+  if (n <= 64) f(integral_constant<int, 64>(), one);
+  else if (n <= 128) f(integral_constant<int, 64>(), two);
+  else if (n <= 256) f(integral_constant<int, 256>(), one);
+  else if (n <= 512) f(integral_constant<int, 256>(), two);
+  else if (n <= 1024) f(most, two);
+  else if (n <= 2048) f(most, integral_constant<int, 4>());
+  else if (sizeof(T) == 4 && n <= 4096) f(most, integral_constant<int, sizeof(T) == 4 ? 8 : 4>());
+  else return false;
+  return true;
 }
-
-template <typename T, int V>
-bool norm_held(const NormArgs& a, hipStream_t s) {
-  const int64_t n = a.width / V;
-  auto go = [&](auto kernel, int rows) {
-    hipLaunchKernelGGL(kernel, flat_grid((a.rows + rows - 1) / rows), dim3(256), 0, s, a);
-    return true;
-  };
-  // a wave a row where there are rows enough for all units
-  if (a.rows >= 1024) {
-    if (n <= 64) return go(norm_kernel<T, V, 1, 64>, 4);
-    if (n <= 128) return go(norm_kernel<T, V, 2, 64>, 4);
-    if (n <= 256) return go(norm_kernel<T, V, 4, 64>, 4);
-    if (n <= 512) return go(norm_kernel<T, V, 8, 64>, 4);
-  }
-  if (n <= 256) return go(norm_kernel<T, V, 1, 256>, 1);
-  if (n <= 512) return go(norm_kernel<T, V, 2, 256>, 1);
-  if (n <= 1024) return go(norm_kernel<T, V, 4, 256>, 1);
-  if (n <= 2048) return go(norm_kernel<T, V, 8, 256>, 1);
-  if constexpr (V == 1)
-    if (n <= 4096) return go(norm_kernel<T, V, 16, 256>, 1);
-  return false;
+template <typename T>
+int64_t packs(int64_t width) {
+  return (width * int64_t(sizeof(T)) + 15) / 16;
+}
+// Workgroups that walk `rows` rows, `side` of them side by side: no more than are resident,
+// and for the gradients no more than leave a share of dw and db worth adding up.
+int64_t walkers(int64_t rows, int side, int64_t most) {
+  return std::max<int64_t>(1, std::min<int64_t>(most, (rows + side - 1) / side));
 }
 
 template <typename T>
 int norm_t(const NormArgs& a, hipStream_t s, std::string* err) {
-  constexpr int V = 16 / int(sizeof(T));
-  const bool wide = a.width % V == 0 && on_grid<T>(a.x, a.ld_x) && on_grid<T>(a.residual, a.ld_residual) &&
-                    on_grid<T>(a.out, a.ld_out) && on_grid<T>(a.total, a.ld_total) && on_grid<T>(a.weight, 0) &&
-                    on_grid<T>(a.bias, 0);
-  if (!(wide ? norm_held<T, V>(a, s) : norm_held<T, 1>(a, s)))
-    hipLaunchKernelGGL(norm_long_kernel<T>, flat_grid(a.rows), dim3(1024), 0, s, a);
+  const bool held = by_width<T>(packs<T>(a.width), [&](auto threads, auto each) {
+    constexpr int R = decltype(threads)::value, Held = decltype(each)::value;
+    hipLaunchKernelGGL((norm_kernel<T, Held, R>),
+                       dim3(unsigned(walkers(a.rows, Sharing<R>::kRows, 256 * 1024 / Sharing<R>::kThreads))),
+                       dim3(Sharing<R>::kThreads), 0, s, a);
+  });
+  if (!held) hipLaunchKernelGGL(norm_long_kernel<T>, flat_grid(a.rows), dim3(1024), 0, s, a);
   return hip_status("layer norm launch", err);
 }
 
-// Workgroups that walk the rows.
-int64_t walkers(int64_t rows) { return std::max<int64_t>(1, std::min<int64_t>(512, (rows + 3) / 4)); }
-int64_t band_height(int64_t rows) { return std::max<int64_t>(64, (rows + 511) / 512); }
-
-template <typename T, int V>
-bool norm_backward_held(const NormArgs& a, hipStream_t s) {
-  const int64_t n = a.width / V;
-  auto go = [&](auto kernel, int threads) {
-    hipLaunchKernelGGL(kernel, dim3(unsigned(walkers(a.rows))), dim3(threads), 0, s, a);
-    return true;
-  };
-  if (n <= 256) return go(norm_backward_kernel<T, V, 1, 256>, 256);
-  if (n <= 512) return go(norm_backward_kernel<T, V, 2, 256>, 256);
-  if (n <= 1024) return go(norm_backward_kernel<T, V, 2, 512>, 512);
-  if (n <= 2048) return go(norm_backward_kernel<T, V, 2, 1024>, 1024);
-  if constexpr (V == 1)
-    if (n <= 4096) return go(norm_backward_kernel<T, V, 4, 1024>, 1024);
-  return false;
-}
+constexpr int64_t kMostShares = 512, kRowsEach = 4;
+int64_t band_height(int64_t rows) { return std::max<int64_t>(64, (rows + kMostShares - 1) / kMostShares); }
 
 template <typename T>
 int norm_backward_t(const NormArgs& args, hipStream_t s, std::string* err) {
-  constexpr int V = 16 / int(sizeof(T));
   NormArgs a = args;
   const bool sums = a.dweight || a.dbias;
   if (!sums) a.partial = nullptr;
-  const bool wide = a.width % V == 0 && on_grid<T>(a.x, a.ld_x) && on_grid<T>(a.dout, a.ld_out) &&
-                    on_grid<T>(a.dtotal, a.ld_dtotal) && on_grid<T>(a.dx, a.ld_dx) && on_grid<T>(a.weight, 0);
-  int64_t shares = walkers(a.rows);
-  if (a.rows > 0 && !(wide ? norm_backward_held<T, V>(a, s) : norm_backward_held<T, 1>(a, s))) {
-    if (a.dx) hipLaunchKernelGGL(norm_backward_long_kernel<T>, flat_grid(a.rows), dim3(1024), 0, s, a);
-    const int64_t height = band_height(a.rows);
-    shares = (a.rows + height - 1) / height;
-    if (sums)
-      hipLaunchKernelGGL(norm_columns_kernel<T>, dim3(unsigned(shares), unsigned((a.width + 255) / 256)), dim3(256), 0, s,
-                         a, height);
+  int64_t shares = 0;
+  if (a.rows > 0) {
+    const bool held = by_width<T>(packs<T>(a.width), [&](auto threads, auto each) {
+      constexpr int R = decltype(threads)::value, Held = decltype(each)::value;
+      shares = walkers((a.rows + kRowsEach - 1) / kRowsEach, Sharing<R>::kRows, kMostShares / (R > 256 ? 2 : 1));
+      hipLaunchKernelGGL((norm_backward_kernel<T, Held, R>), dim3(unsigned(shares)), dim3(Sharing<R>::kThreads), 0, s, a);
+    });
+    if (!held) {
+      if (a.dx) hipLaunchKernelGGL(norm_backward_long_kernel<T>, flat_grid(a.rows), dim3(1024), 0, s, a);
+      const int64_t height = band_height(a.rows);
+      shares = (a.rows + height - 1) / height;
+      if (sums)
+        hipLaunchKernelGGL(norm_columns_kernel<T>, dim3(unsigned(shares), unsigned((a.width + 255) / 256)), dim3(256), 0,
+                           s, a, height);
+    }
   }
   if (sums)
-    hipLaunchKernelGGL(norm_sum_kernel<T>, dim3(unsigned((a.width + 63) / 64), 2), dim3(1024), 0, s, a,
-                       a.rows > 0 ? shares : 0);
+    hipLaunchKernelGGL(norm_sum_kernel<T>, dim3(unsigned((a.width + 63) / 64), 2), dim3(1024), 0, s, a, shares);
   return hip_status("layer norm gradient launch", err);
 }
 
@@ -522,10 +586,7 @@ int launch_norm(int dtype, const NormArgs& args, void* stream, std::string* err)
   return dtype == CCL_BF16 ? prod::norm_t<prod::bf16>(args, s, err) : prod::norm_t<float>(args, s, err);
 }
 
-int64_t norm_partials(int64_t rows, int64_t) {
-  const int64_t height = prod::band_height(rows);
-  return std::max(prod::walkers(rows), (rows + height - 1) / height);
-}
+int64_t norm_partials(int64_t rows) { return std::max<int64_t>(1, std::min<int64_t>(prod::kMostShares, rows)); }
 
 int launch_norm_backward(int dtype, const NormArgs& args, void* stream, std::string* err) {
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);

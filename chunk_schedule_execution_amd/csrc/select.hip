@@ -1,9 +1,11 @@
 // The choice of experts for gfx950: scores, groups, the highest `choices` of a token's
 // experts and their gates, and the gradient of the gates.
 //
-// L lanes take a token (16 up to 256 experts, 64 above), lane l its experts l, L + l, ... in
-// registers. A choice is a maximum over the lane's values, one over the lanes, and the
-// lowest index that has it; the chosen one leaves. No token waits for another.
+// What has to be right to the last bit is the order of p + bias in 64 bits; what would be
+// slow is computing all of it there. So 16 lanes take a token, each its experts l, 16 + l, ...
+// in registers, and find in fp32 the few experts that may be among the highest: those not
+// below the choices-th highest of the lanes' maxima, less what fp32 may be off. Only their
+// values are computed in 64 bits, one per lane, and each counts how many come before it.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -17,15 +19,23 @@ namespace prod {
 namespace {
 
 constexpr int kThreads = 256, kMaxChoices = 64, kMaxGroups = 64;
-
 constexpr float kClosed = -INFINITY;
+
+// exp to two steps of fp32: the argument's rounding on its way to a power of 2 is carried
+// along. NaN stays; beyond +-200 the result is 0 or infinite either way.
+__device__ inline float exp_exact(float x) {
+  x = x < -200.0f ? -200.0f : x > 200.0f ? 200.0f : x;
+  const float t = x * 1.44269504088896341f;
+  const float rest = fmaf(x, 1.44269504088896341f, -t) + x * 1.92596299e-8f;
+  return __builtin_amdgcn_exp2f(t) * fmaf(rest, 0.693147180559945309f, 1.0f);
+}
 
 // A score times a factor that the chosen experts of a token share: exp(-m) for softmax (m
 // their highest logit, or the row's), exp(-m) with m = min(0, highest) for sigmoid, so that a
 // ratio of scores is right also where the scores themselves are too small for fp32. m = 0
 // gives the sigmoid itself.
 __device__ inline float scaled_score(float x, float m, bool soft) {
-  return soft ? expf(x - m) : 1.0f / (expf(m) + expf(m - x));
+  return soft ? exp_exact(x - m) : 1.0f / (exp_exact(m) + exp_exact(m - x));
 }
 __device__ inline float shared_top(float highest, bool soft) {
   return highest == -INFINITY ? 0.0f : soft ? highest : fminf(0.0f, highest);
@@ -41,126 +51,130 @@ __device__ inline float row_top(const float (&x)[NE]) {
   return m == kClosed ? 0.0f : m;
 }
 
-template <typename T, int L, int NE>
-__device__ inline void load_row(const SelectArgs& a, int64_t t, int lane, float (&x)[NE]) {
-  const T* row = static_cast<const T*>(a.logits) + t * a.ld;
+// Which expert a lane's value i is: V neighbours of each 16-byte (or shorter) vector in turn,
+// a quarter of the lanes further with every vector, so that the experts of a group, which are
+// neighbours, fall to all lanes about equally.
+template <int L, int V>
+__device__ inline int expert_at(int i, int lane) {
+  return V == 1 ? i * L + lane : i / V * (L * V) + ((lane + i / V * (L / 4)) & (L - 1)) * V + i % V;
+}
+// V > 1: row and ends lie on the grid of V values.
+template <int L, int V, int NE, typename T>
+__device__ inline void load_row(const T* row, int lane, int experts, float fill, float (&x)[NE]) {
+  typedef T pack __attribute__((ext_vector_type(V)));
 #pragma unroll
-  for (int i = 0; i < NE; ++i) {
-    const int e = i * L + lane;
-    x[i] = t < a.tokens && e < a.experts ? widen(row[e]) : kClosed;
+  for (int i = 0; i < NE; i += V) {
+    const int e = expert_at<L, V>(i, lane);
+    if constexpr (V == 1) {
+      x[i] = e < experts ? widen(row[e]) : fill;
+    } else {
+      pack v = {};
+      if (e < experts) v = *reinterpret_cast<const pack*>(row + e);
+#pragma unroll
+      for (int q = 0; q < V; ++q) x[i + q] = e < experts ? widen(v[q]) : fill;
+    }
   }
 }
 
-// ---- the choice ----------------------------------------------------------------------------
-// Takes the keys of experts outside the kept groups away. A lane takes a group, in LDS.
-template <typename Key, int L, int NE>
-struct Groups {
-  Key value[kThreads / L][L * NE];
-  Key best[kThreads / L][kMaxGroups];
-  bool kept[kThreads / L][kMaxGroups];
+// What an expert is ranked by, in 64 bits. total: of the row's exp(x - top), softmax only.
+__device__ inline double score_of(float x, float top, double total, bool soft) {
+  return soft ? exp(double(x) - double(top)) / total : 1.0 / (1.0 + exp(-double(x)));
+}
+template <typename V>
+__device__ inline V nan_first(V v) {
+  return v == v ? v : V(INFINITY);
+}
 
-  __device__ inline void keep(const SelectArgs& a, int slot, int lane, const Key (&v)[NE], Key (&key)[NE]) {
-    const int per = a.experts / a.groups;
+// Which groups stay: a group's value is that of its best experts; ties go to the lower group.
+template <typename V>
+__device__ inline int groups_before(const V* best, int groups, int g) {
+  int before = 0;
+  for (int h = 0; h < groups; ++h) before += best[h] > best[g] || (best[h] == best[g] && h < g);
+  return before;
+}
+// The group of expert e < 2^10, by magic = 2^20 / per + 1: without a division.
+__device__ inline int group_of(int e, int magic) { return int(__umul24(e, magic) >> 20); }
+
+// ---- a wave for a token -----------------------------------------------------------------------
+template <int NE>
+struct WholeSpace {
+  double value[64 * NE];
+  double best[kMaxGroups];
+  bool kept[kMaxGroups];
+};
+
+// The choice by maxima in turn, all in 64 bits: for more experts or choices than 16 lanes
+// take, and for tokens whose order fp32 could not tell.
+template <typename T, int NE>
+__device__ inline void choose_whole(const SelectArgs& a, int64_t t, WholeSpace<NE>& space, int* chosen) {
+  const int lane = threadIdx.x & 63;
+  const double closed = kClosed;
+  float x[NE];
+  load_row<64, 1>(static_cast<const T*>(a.logits) + t * a.ld, lane, a.experts, kClosed, x);
+  const bool soft = a.score == CCL_SCORE_SOFTMAX, grouped = a.kept < a.groups;
+  const bool scored = a.bias || (grouped && a.best == 2);
+  const float top = row_top<64>(x);
+  double total = 0.0;
+  if (scored && soft) {
 #pragma unroll
-    for (int i = 0; i < NE; ++i) value[slot][i * L + lane] = v[i];
+    for (int i = 0; i < NE; ++i) total += exp(double(x[i]) - double(top));
+    total = over_sum<64>(total);
+  }
+  double key[NE];
+#pragma unroll
+  for (int i = 0; i < NE; ++i) {
+    const int e = i * 64 + lane;
+    const float b = a.bias && e < a.experts ? a.bias[e] : 0.0f;
+    double v = nan_first(double(x[i]));
+    if (scored) v = nan_first(score_of(x[i], top, total, soft) + double(b));
+    if (x[i] == kClosed || b == kClosed) v = closed;
+    if (grouped) space.value[e] = v;
+    key[i] = a.bias || v == closed ? v : nan_first(double(x[i]));
+  }
+  if (grouped) {
+    const int per = a.per;
     __builtin_amdgcn_wave_barrier();
-    for (int g = lane; g < a.groups; g += L) {
-      Key first = kClosed, second = kClosed;
+    double first = closed, second = closed;
+    if (lane < a.groups)
       for (int q = 0; q < per; ++q) {
-        const Key w = value[slot][g * per + q];
+        const double w = space.value[lane * per + q];
         second = w > first ? first : w > second ? w : second;
         first = w > first ? w : first;
       }
-      best[slot][g] = a.best == 2 && second > Key(kClosed) ? first + second : first;
-    }
+    space.best[lane] = a.best == 2 && second > closed ? first + second : first;
     __builtin_amdgcn_wave_barrier();
-    for (int g = lane; g < a.groups; g += L) {
-      const Key mine = best[slot][g];
-      int before = 0;
-      for (int h = 0; h < a.groups; ++h) before += best[slot][h] > mine || (best[slot][h] == mine && h < g);
-      kept[slot][g] = before < a.kept;
-    }
+    if (lane < a.groups) space.kept[lane] = groups_before(space.best, a.groups, lane) < a.kept;
     __builtin_amdgcn_wave_barrier();
-    // e / per without a division: e and per are at most 2^10
-    const unsigned magic = (1u << 20) / per + 1;
 #pragma unroll
     for (int i = 0; i < NE; ++i) {
-      const unsigned e = i * L + lane;
-      if (e < unsigned(a.experts) && !kept[slot][e * magic >> 20]) key[i] = kClosed;
+      const int e = i * 64 + lane;
+      if (e < a.experts && !space.kept[group_of(e, a.magic)]) key[i] = closed;
     }
   }
-};
-struct NoGroups {};
-
-// Key double: scores and bias are added and compared in 64 bits, since fp32 would take the
-// wrong one of two experts a rounding apart. Key float: the logits themselves are compared
-// (no bias: the scores rise with them).
-template <typename T, typename Key, bool Grouped, int L, int NE>
-__global__ __launch_bounds__(kThreads) void select_kernel(SelectArgs a) {
-  constexpr bool Scored = std::is_same<Key, double>::value;
-  __shared__ int chosen[kThreads / L][kMaxChoices];
-  __shared__ typename std::conditional<Grouped, Groups<Key, L, NE>, NoGroups>::type groups;
-  const int lane = threadIdx.x % L, slot = threadIdx.x / L;
-  const int64_t t = (int64_t(blockIdx.y) * gridDim.x + blockIdx.x) * (kThreads / L) + slot;
-  const Key closed = Key(kClosed);
-  float x[NE];
-  load_row<T, L>(a, t, lane, x);
-  const float top = row_top<L>(x);
-
-  Key key[NE];
-  if constexpr (Scored) {
-    double v[NE], total = 0.0;
-    const bool soft = a.score == CCL_SCORE_SOFTMAX;
-#pragma unroll
-    for (int i = 0; i < NE; ++i) {
-      v[i] = soft ? exp(double(x[i]) - double(top)) : 1.0 / (1.0 + exp(-double(x[i])));
-      total += v[i];
-    }
-    if (soft) {
-      total = over_sum<L>(total);
-#pragma unroll
-      for (int i = 0; i < NE; ++i) v[i] /= total;
-    }
-#pragma unroll
-    for (int i = 0; i < NE; ++i) {
-      const int e = i * L + lane;
-      if (a.bias) v[i] += e < a.experts ? double(a.bias[e]) : 0.0;
-      if (!(v[i] == v[i])) v[i] = INFINITY;
-      if (x[i] == kClosed || (a.bias && e < a.experts && a.bias[e] == kClosed)) v[i] = closed;
-      key[i] = a.bias || v[i] == closed ? v[i] : x[i] == x[i] ? double(x[i]) : INFINITY;
-    }
-    if constexpr (Grouped) groups.keep(a, slot, lane, v, key);
-  } else {
-#pragma unroll
-    for (int i = 0; i < NE; ++i) key[i] = x[i] == x[i] ? x[i] : INFINITY;
-    if constexpr (Grouped) {
-      Key v[NE];
-#pragma unroll
-      for (int i = 0; i < NE; ++i) v[i] = key[i];
-      groups.keep(a, slot, lane, v, key);
-    }
-  }
-
   for (int c = 0; c < a.choices; ++c) {
-    Key m = closed;
+    double m = closed;
     int at = a.experts;
 #pragma unroll
     for (int i = 0; i < NE; ++i)
       if (key[i] > m) {
         m = key[i];
-        at = i * L + lane;
+        at = i * 64 + lane;
       }
-    const Key best = over_max<L>(m);
-    const int first = over<L>(m == best ? at : a.experts, [](int p, int q) { return min(p, q); });
-    if (lane == 0) chosen[slot][c] = first < a.experts ? first : -1;
+    const double best = over_max<64>(m);
+    const int first = over<64>(m == best ? at : a.experts, [](int p, int q) { return min(p, q); });
+    if (lane == 0) chosen[c] = first < a.experts ? first : -1;
 #pragma unroll
     for (int i = 0; i < NE; ++i)
-      if (first == i * L + lane) key[i] = closed;
+      if (first == i * 64 + lane) key[i] = closed;
   }
   __builtin_amdgcn_wave_barrier();
+}
 
-  // gates: of the chosen logits, read again (they are in the caches)
-  constexpr int Each = kMaxChoices / L;
+// ---- gates -----------------------------------------------------------------------------------
+// Of the chosen logits, read again (they are in the caches). x, top: the row, its maximum.
+template <typename T, int L, int Each, int NE>
+__device__ inline void write_gates(const SelectArgs& a, int64_t t, int lane, const int* chosen, const float (&x)[NE],
+                                   float top) {
   const bool soft = a.score == CCL_SCORE_SOFTMAX;
   const T* row = static_cast<const T*>(a.logits) + t * a.ld;
   int id[Each];
@@ -168,7 +182,7 @@ __global__ __launch_bounds__(kThreads) void select_kernel(SelectArgs a) {
 #pragma unroll
   for (int j = 0; j < Each; ++j) {
     const int c = j * L + lane;
-    id[j] = c < a.choices && t < a.tokens ? chosen[slot][c] : -1;
+    id[j] = c < a.choices && t < a.tokens ? chosen[c] : -1;
     q[j] = id[j] >= 0 ? widen(row[id[j]]) : kClosed;
     m = fmaxf(m, q[j]);
   }
@@ -184,7 +198,7 @@ __global__ __launch_bounds__(kThreads) void select_kernel(SelectArgs a) {
   } else if (soft) {
     total = 0.0f;
 #pragma unroll
-    for (int i = 0; i < NE; ++i) total += expf(x[i] - m);
+    for (int i = 0; i < NE; ++i) total += exp_exact(x[i] - top);
     total = over_sum<L>(total);
   }
 #pragma unroll
@@ -196,16 +210,253 @@ __global__ __launch_bounds__(kThreads) void select_kernel(SelectArgs a) {
   }
 }
 
+template <typename T, int NE>
+__global__ __launch_bounds__(kThreads) void select_whole_kernel(SelectArgs a) {
+  __shared__ WholeSpace<NE> space[kThreads / 64];
+  __shared__ int chosen[kThreads / 64][kMaxChoices];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t t = (int64_t(blockIdx.y) * gridDim.x + blockIdx.x) * (kThreads / 64) + wave;
+  if (t >= a.tokens) return;  // a whole wave
+  choose_whole<T, NE>(a, t, space[wave], chosen[wave]);
+  float x[NE];
+  load_row<64, 1>(static_cast<const T*>(a.logits) + t * a.ld, lane, a.experts, kClosed, x);
+  write_gates<T, 64, 1>(a, t, lane, chosen[wave], x, row_top<64>(x));
+}
+
+// ---- 16 lanes for a token ----------------------------------------------------------------------
+constexpr int kCandidates = 48;
+// Choices that the kernel of 16 lanes takes: beyond, more experts than kCandidates reach the
+// choices-th highest of 16 maxima too often.
+constexpr int kFewChoices = 12;
+constexpr int kFewGroups = 32;  // a word of bits
+
+// LDS of a wave: four tokens.
+template <int NE>
+struct FewSpace {
+  static constexpr int kRow = 18 * NE + 2;  // four values more every 32: groups of 32 in different banks
+  int chosen[4][16];
+  int whole_chosen[kMaxChoices];
+  double value[4][kCandidates];
+  int expert[4][kCandidates];
+  union {
+    struct {
+      float value[4][kRow];
+      float best[4][kFewGroups];
+    } groups;
+    WholeSpace<(NE + 3) / 4> whole;
+  };
+  static __device__ inline int at(int e) { return e + (e >> 5) * 4; }
+};
+
+// What a value in fp32 may be off by, but for the addition of its bias (2^-24 of the sum). The
+// exponential's argument: p |x| 2^-24 with p |x| < 0.4; a step or two of p for the functions;
+// in a softmax, one for each of the sum's 20 additions.
+__device__ inline float value_off(bool soft) { return soft ? 0x1p-19f : 0x1p-21f; }
+
+// Takes the keys of experts outside the kept groups away; true where fp32 cannot tell which
+// those are. v: the experts' values, exact where they are the logits.
+template <bool Scored, int V, int NE>
+__device__ inline bool keep_groups(const SelectArgs& a, FewSpace<NE>& space, int token, int lane, const float (&v)[NE],
+                                   float (&key)[NE]) {
+  auto& s = space.groups;
+  const int groups = a.groups, parts = 1 << a.parts_log2;
+#pragma unroll
+  for (int i = 0; i < NE; ++i) s.value[token][space.at(expert_at<16, V>(i, lane))] = v[i];
+  __builtin_amdgcn_wave_barrier();
+  // the lanes share out the groups, or parts of a group where those are few
+  for (int j = lane; j < groups * parts; j += 16) {
+    const int g = j >> a.parts_log2, end = g * a.per + a.per;
+    float first = kClosed, second = kClosed;
+#pragma unroll 4
+    for (int e = g * a.per + (j & (parts - 1)); e < end; e += parts) {
+      const float w = s.value[token][space.at(e)];
+      second = fmaxf(second, fminf(first, w));
+      first = fmaxf(first, w);
+    }
+    for (int p = 1; p < parts; p *= 2) {  // groups x parts lanes, all of them here
+      const float w = __shfl_xor(first, p), u = __shfl_xor(second, p);
+      second = fmaxf(fmaxf(second, u), fminf(first, w));
+      first = fmaxf(first, w);
+    }
+    s.best[token][g] = a.best == 2 && second > kClosed ? first + second : first;
+  }
+  __builtin_amdgcn_wave_barrier();
+  float lowest = INFINITY, highest = kClosed;  // of the groups that stay, of the others
+  unsigned kept = 0;
+  for (int g = lane; g < 16 * ((groups + 15) / 16); g += 16) {
+    const bool stays = g < groups && groups_before(s.best[token], groups, g) < a.kept;
+    if (stays) lowest = fminf(lowest, s.best[token][g]);
+    else if (g < groups) highest = fmaxf(highest, s.best[token][g]);
+    kept |= (unsigned(__ballot(stays) >> (token * 16)) & 0xffff) << (g & 16);
+  }
+  // (past the last expert keys are closed already)
+  if (V > 1 && a.per % V == 0) {  // whole vectors
+#pragma unroll
+    for (int i = 0; i < NE; i += V) {
+      const bool out = !(kept >> group_of(expert_at<16, V>(i, lane), a.magic) & 1);
+#pragma unroll
+      for (int q = 0; q < V; ++q) key[i + q] = out ? kClosed : key[i + q];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NE; ++i)
+      if (!(kept >> group_of(expert_at<16, V>(i, lane), a.magic) & 1)) key[i] = kClosed;
+  }
+  if (!Scored) return false;
+  lowest = -over_max<16>(-lowest);
+  highest = over_max<16>(highest);
+  // sums of two values on either side
+  return highest > kClosed && !(lowest - highest > 4 * value_off(a.score == CCL_SCORE_SOFTMAX) + 0x1p-21f * fabsf(highest));
+}
+
+// Scored: experts are ranked by p + bias, or groups by sums of p. Otherwise by their logits,
+// which fp32 holds as they are.
+template <typename T, bool Scored, bool Grouped, int NE, int V>
+__global__ __launch_bounds__(kThreads) void select_kernel(SelectArgs a) {
+  __shared__ FewSpace<NE> spaces[kThreads / 64];
+  FewSpace<NE>& space = spaces[threadIdx.x >> 6];
+  const int lane = threadIdx.x & 15, token = (threadIdx.x & 63) >> 4;
+  const int64_t t0 = (int64_t(blockIdx.y) * gridDim.x + blockIdx.x) * (kThreads / 16) + (threadIdx.x >> 6) * 4;
+  const int64_t t = t0 + token;
+  const bool soft = a.score == CCL_SCORE_SOFTMAX;
+  const T* row = static_cast<const T*>(a.logits) + t * a.ld;
+  float x[NE];
+  load_row<16, V>(row, lane, t < a.tokens ? a.experts : 0, kClosed, x);
+  const float top = soft ? row_top<16>(x) : 0.0f;
+
+  double total = 0.0;  // softmax with a bias: the sum is part of what is compared
+  float key[NE];
+  bool doubt = false;
+  if constexpr (Scored) {
+    float v[NE], lower[NE], sum = 0.0f;  // lower: of the logit and the bias, -inf where one is
+    if (soft) {
+#pragma unroll
+      for (int i = 0; i < NE; ++i) {
+        v[i] = __builtin_amdgcn_exp2f((x[i] - top) * 1.44269504088896341f);
+        sum += v[i];
+      }
+      sum = over_sum<16>(sum);
+      const float inverse = sum != 0.0f ? reciprocal(sum) : 0.0f;  // 0: all closed
+#pragma unroll
+      for (int i = 0; i < NE; ++i) v[i] *= inverse;
+    } else {
+#pragma unroll
+      for (int i = 0; i < NE; ++i) v[i] = reciprocal(1.0f + __builtin_amdgcn_exp2f(x[i] * -1.44269504088896341f));
+    }
+    sum = 0.0f;
+    if (a.bias) {
+      float b[NE];
+      load_row<16, V>(a.bias, lane, a.experts, 0.0f, b);
+#pragma unroll
+      for (int i = 0; i < NE; ++i) {
+        v[i] += b[i];
+        key[i] = v[i];
+        sum += v[i];
+        lower[i] = fminf(x[i], b[i]);
+      }
+      if (soft) {
+#pragma unroll
+        for (int i = 0; i < NE; ++i) total += exp(double(x[i]) - double(top));
+        total = over_sum<16>(total);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NE; ++i) {
+        key[i] = lower[i] = x[i];
+        sum += v[i];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < NE; ++i)
+      if (lower[i] == kClosed) key[i] = v[i] = kClosed;
+    doubt = !(sum == sum);  // a NaN somewhere
+    if constexpr (Grouped) doubt = keep_groups<Scored, V>(a, space, token, lane, v, key) || doubt;
+  } else {
+#pragma unroll
+    for (int i = 0; i < NE; ++i) key[i] = nan_first(x[i]);
+    if constexpr (Grouped) {
+      float v[NE];
+#pragma unroll
+      for (int i = 0; i < NE; ++i) v[i] = key[i];
+      keep_groups<Scored, V>(a, space, token, lane, v, key);
+    }
+  }
+
+  // the choices-th highest of the lanes' maxima: at least `choices` experts reach it
+  float most = key[0];
+#pragma unroll
+  for (int i = 1; i < NE; ++i) most = fmaxf(most, key[i]);
+  int above = 0;
+#define CCL_MEET(N) above += turned<N>(most) > most;
+  CCL_MEET(1) CCL_MEET(2) CCL_MEET(3) CCL_MEET(4) CCL_MEET(5) CCL_MEET(6) CCL_MEET(7) CCL_MEET(8)
+  CCL_MEET(9) CCL_MEET(10) CCL_MEET(11) CCL_MEET(12) CCL_MEET(13) CCL_MEET(14) CCL_MEET(15)
+#undef CCL_MEET
+  float reach = -over_max<16>(above < a.choices ? -most : kClosed);
+  if (Scored && a.bias && fabsf(reach) < INFINITY) reach -= 2 * value_off(soft) + 0x1p-22f * fabsf(reach);
+  reach = fmaxf(reach, -__FLT_MAX__);  // closed ones never do
+
+  // their numbers, lane by lane
+  unsigned hits = 0;
+#pragma unroll
+  for (int i = 0; i < NE; ++i) hits |= key[i] >= reach ? 1u << i : 0u;
+  const int mine = __popc(hits);
+  int place = mine;  // up to and with this lane's
+#define CCL_UPTO(N) place += __builtin_amdgcn_update_dpp(0, place, 0x110 + N, 0xf, 0xf, true);
+  CCL_UPTO(1) CCL_UPTO(2) CCL_UPTO(4) CCL_UPTO(8)
+#undef CCL_UPTO
+  int count = over<16>(place, [](int p, int q) { return max(p, q); });
+  place -= mine;
+  while (hits) {
+    const int i = __ffs(hits) - 1;
+    hits &= hits - 1;
+    if (place < kCandidates) space.expert[token][place] = expert_at<16, V>(i, lane);
+    ++place;
+  }
+  doubt = doubt || count > kCandidates;
+  count = min(count, kCandidates);
+  if (lane >= count && lane < a.choices) space.chosen[token][lane] = -1;
+  __builtin_amdgcn_wave_barrier();
+  for (int c = lane; c < count; c += 16) {
+    const int e = space.expert[token][c];
+    const float logit = widen(row[e]);
+    space.value[token][c] =
+        nan_first(Scored && a.bias ? score_of(logit, top, total, soft) + double(a.bias[e]) : double(logit));
+  }
+  __builtin_amdgcn_wave_barrier();
+  for (int c = lane; c < count; c += 16) {
+    const double v = space.value[token][c];
+    const int e = space.expert[token][c];
+    int rank = 0;
+    for (int d = 0; d < count; ++d) {
+      const double w = space.value[token][d];
+      rank += w > v || (w == v && space.expert[token][d] < e);
+    }
+    if (rank < a.choices) space.chosen[token][rank] = e;
+  }
+  __builtin_amdgcn_wave_barrier();
+
+  const unsigned long long doubts = __ballot(doubt && t < a.tokens);
+  if (doubts) {
+#pragma nounroll
+    for (int j = 0; j < 4; ++j) {
+      if (!((doubts >> (j * 16)) & 0xffff)) continue;
+      choose_whole<T, (NE + 3) / 4>(a, t0 + j, space.whole, space.whole_chosen);
+      if (token == j && lane < a.choices) space.chosen[j][lane] = space.whole_chosen[lane];
+      __builtin_amdgcn_wave_barrier();
+    }
+  }
+  write_gates<T, 16, 1>(a, t, lane, space.chosen[token], x, top);
+}
+
 // ---- the gradient --------------------------------------------------------------------------
 // dx_e = p_e (d_e - sum p d) for softmax, d_e p_e (1 - p_e) for sigmoid, d the scores'
 // gradients, zero but at the chosen experts; where the gates were divided by their sum the
 // others have no part in them. The gradients of choices with the same id are added in their
 // order.
-template <typename T, int L, int NE>
+template <typename T, int L, int NE, int V, int Each>
 __global__ __launch_bounds__(kThreads) void select_backward_kernel(SelectArgs a) {
-  constexpr int Each = kMaxChoices / L;
-  __shared__ int chosen[kThreads / L][kMaxChoices];
-  __shared__ float grad[kThreads / L][kMaxChoices];
+  __shared__ int chosen[kThreads / L][L * Each];
+  __shared__ float grad[kThreads / L][L * Each];
   __shared__ float spread[kThreads / L][L * NE];
   const int lane = threadIdx.x % L, slot = threadIdx.x / L;
   const int64_t t = (int64_t(blockIdx.y) * gridDim.x + blockIdx.x) * (kThreads / L) + slot;
@@ -213,19 +464,19 @@ __global__ __launch_bounds__(kThreads) void select_backward_kernel(SelectArgs a)
   const T* row = static_cast<const T*>(a.logits) + t * a.ld;
   float x[NE], m = 0.0f, total = 1.0f;
   if (whole) {  // p of every expert
-    load_row<T, L>(a, t, lane, x);
+    load_row<L, V>(row, lane, t < a.tokens ? a.experts : 0, kClosed, x);
     m = row_top<L>(x);
     total = 0.0f;
 #pragma unroll
     for (int i = 0; i < NE; ++i) {
-      x[i] = expf(x[i] - m);
+      x[i] = exp_exact(x[i] - m);
       total += x[i];
     }
     total = over_sum<L>(total);
     if (total == 0.0f) total = 1.0f;
   }
 #pragma unroll
-  for (int i = 0; i < NE; ++i) spread[slot][i * L + lane] = 0.0f;
+  for (int i = 0; i < NE; ++i) spread[slot][expert_at<L, V>(i, lane)] = 0.0f;
 
   int id[Each];
   float d[Each], p[Each], xs[Each];
@@ -290,10 +541,16 @@ __global__ __launch_bounds__(kThreads) void select_backward_kernel(SelectArgs a)
   __builtin_amdgcn_wave_barrier();
   if (t >= a.tokens) return;
   T* out = static_cast<T*>(a.dlogits) + t * a.ldd;
+  const float share = whole ? flow / total : 0.0f;
+  typedef T pack __attribute__((ext_vector_type(V)));
 #pragma unroll
-  for (int i = 0; i < NE; ++i) {
-    const int e = i * L + lane;
-    if (e < a.experts) out[e] = narrow<T>(spread[slot][e] - (whole ? x[i] / total * flow : 0.0f));
+  for (int i = 0; i < NE; i += V) {
+    const int e = expert_at<L, V>(i, lane);
+    if (e >= a.experts) continue;
+    pack o;
+#pragma unroll
+    for (int q = 0; q < V; ++q) o[q] = narrow<T>(whole ? fmaf(-x[i + q], share, spread[slot][e + q]) : spread[slot][e + q]);
+    *reinterpret_cast<pack*>(out + e) = o;
   }
 }
 
@@ -307,25 +564,49 @@ dim3 token_grid(int64_t tokens) {
 template <typename F>
 void by_experts(int experts, F f) {
   using std::integral_constant;
-  auto with = [&](auto lanes, auto each) { f(lanes, each); };
-  if (experts <= 32) with(integral_constant<int, 16>(), integral_constant<int, 2>());
-  else if (experts <= 64) with(integral_constant<int, 16>(), integral_constant<int, 4>());
-  else if (experts <= 128) with(integral_constant<int, 16>(), integral_constant<int, 8>());
-  else if (experts <= 256) with(integral_constant<int, 16>(), integral_constant<int, 16>());
-  else if (experts <= 512) with(integral_constant<int, 64>(), integral_constant<int, 8>());
-  else with(integral_constant<int, 64>(), integral_constant<int, 16>());
+  const integral_constant<int, 16> few;
+  const integral_constant<int, 64> wave;
+  if (experts <= 32) f(few, integral_constant<int, 2>());
+  else if (experts <= 64) f(few, integral_constant<int, 4>());
+  else if (experts <= 128) f(few, integral_constant<int, 8>());
+  else if (experts <= 256) f(few, integral_constant<int, 16>());
+  else if (experts <= 512) f(wave, integral_constant<int, 8>());
+  else f(wave, integral_constant<int, 16>());
+}
+
+// Whether rows of `experts` values are whole vectors of V.
+template <typename T, int V>
+bool on_grid(const void* p, int64_t ld, int experts) {
+  return reinterpret_cast<uintptr_t>(p) % (V * sizeof(T)) == 0 && ld % V == 0 && experts % V == 0;
+}
+template <typename T, int NE>
+constexpr int vector_of() {
+  return NE < 16 / int(sizeof(T)) ? NE : 16 / int(sizeof(T));
+}
+
+template <typename T, int NE, int V>
+void select_few(const SelectArgs& a, hipStream_t s) {
+  const bool grouped = a.kept < a.groups, scored = a.bias || (grouped && a.best == 2);
+  auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, token_grid<16>(a.tokens), dim3(kThreads), 0, s, a); };
+  if (scored && grouped) go(select_kernel<T, true, true, NE, V>);
+  else if (scored) go(select_kernel<T, true, false, NE, V>);
+  else if (grouped) go(select_kernel<T, false, true, NE, V>);
+  else go(select_kernel<T, false, false, NE, V>);
 }
 
 template <typename T>
 int select_t(const SelectArgs& a, hipStream_t s, std::string* err) {
-  const bool grouped = a.kept < a.groups, scored = a.bias || (grouped && a.best == 2);
   by_experts(a.experts, [&](auto lanes, auto each) {
     constexpr int L = decltype(lanes)::value, NE = decltype(each)::value;
-    auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, token_grid<L>(a.tokens), dim3(kThreads), 0, s, a); };
-    if (scored && grouped) go(select_kernel<T, double, true, L, NE>);
-    else if (scored) go(select_kernel<T, double, false, L, NE>);
-    else if (grouped) go(select_kernel<T, float, true, L, NE>);
-    else go(select_kernel<T, float, false, L, NE>);
+    auto whole = [&](auto kernel) { hipLaunchKernelGGL(kernel, token_grid<64>(a.tokens), dim3(kThreads), 0, s, a); };
+    if constexpr (L == 16) {
+      constexpr int V = vector_of<T, NE>();
+      if (a.choices > kFewChoices || (a.kept < a.groups && a.groups > kFewGroups)) whole(select_whole_kernel<T, (NE + 3) / 4>);
+      else if (on_grid<T, V>(a.logits, a.ld, a.experts) && reinterpret_cast<uintptr_t>(a.bias) % (V * 4) == 0) select_few<T, NE, V>(a, s);
+      else select_few<T, NE, 1>(a, s);
+    } else {
+      whole(select_whole_kernel<T, NE>);
+    }
   });
   return hip_status("expert selection launch", err);
 }
@@ -333,8 +614,17 @@ int select_t(const SelectArgs& a, hipStream_t s, std::string* err) {
 template <typename T>
 int select_backward_t(const SelectArgs& a, hipStream_t s, std::string* err) {
   by_experts(a.experts, [&](auto lanes, auto each) {
-    constexpr int L = decltype(lanes)::value, NE = decltype(each)::value;
-    hipLaunchKernelGGL((select_backward_kernel<T, L, NE>), token_grid<L>(a.tokens), dim3(kThreads), 0, s, a);
+    constexpr int L = decltype(lanes)::value, NE = decltype(each)::value, V = vector_of<T, NE>();
+    auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, token_grid<L>(a.tokens), dim3(kThreads), 0, s, a); };
+    const bool vec = on_grid<T, V>(a.logits, a.ld, a.experts) && on_grid<T, V>(a.dlogits, a.ldd, a.experts);
+    if constexpr (L == 64) {
+      if (vec) go(select_backward_kernel<T, L, NE, V, 1>);
+      else go(select_backward_kernel<T, L, NE, 1, 1>);
+    } else {
+      if (a.choices > 16) go(select_backward_kernel<T, L, NE, 1, kMaxChoices / L>);
+      else if (vec) go(select_backward_kernel<T, L, NE, V, 1>);
+      else go(select_backward_kernel<T, L, NE, 1, 1>);
+    }
   });
   return hip_status("expert selection gradient launch", err);
 }
