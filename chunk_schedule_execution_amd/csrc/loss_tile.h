@@ -14,8 +14,11 @@ namespace {
 
 constexpr float kLog2e = 1.44269504088896341f;
 
-// exp(v) by the hardware's power of 2: off by 2^-24 of |v| and a step.
-__device__ inline float exp_of(float v) { return __builtin_amdgcn_exp2f(v * kLog2e); }
+// exp(z - base), base2 = base log2(e), by the hardware's power of 2: one rounding of the
+// argument, so off by 2^-24 of |z - base| and of |base| and a step.
+__device__ inline float exp_from(float z, float base2) {
+  return __builtin_amdgcn_exp2f(fmaf(z, kLog2e, -base2));
+}
 
 // Column of a target, negative where there is none.
 __device__ inline int target_column(int target, int first) { return target < 0 ? -1 : max(-1, target - first); }
@@ -68,12 +71,12 @@ struct RowSums {
         for (int q = 0; q < 4; ++q) m = fmaxf(m, acc[i][j][q]);
       m = fmaxf(m, __shfl_xor(m, 16));
       m = fmaxf(m, __shfl_xor(m, 32));
-      const float base = m == -INFINITY ? 0.0f : m;
+      const float base2 = m == -INFINITY ? 0.0f : m * kLog2e;
       float sum = 0.0f;
 #pragma unroll
       for (int j = 0; j < FN; ++j)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) sum += exp_of(acc[i][j][q] - base);
+        for (int q = 0; q < 4; ++q) sum += exp_from(acc[i][j][q], base2);
       sum += __shfl_xor(sum, 16);
       sum += __shfl_xor(sum, 32);
       if (in >= job.m_end - job.row) continue;
@@ -126,15 +129,28 @@ struct LossSlope {
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
       const bool out = rows.at[i] == INT_MIN;
-      const int at = out ? -1 : rows.at[i] - first;
+      const float lse2 = rows.lse[i] * kLog2e;
 #pragma unroll
       for (int j = 0; j < FN; ++j)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int c = held_column(lane, j, q);
-          const float p = exp_of(acc[i][j][q] - rows.lse[i]) - (c == at ? 1.0f : 0.0f);
-          acc[i][j][q] = out || c >= left ? 0.0f : rows.d[i] * p;
-        }
+        for (int q = 0; q < 4; ++q) acc[i][j][q] = out ? 0.0f : rows.d[i] * exp_from(acc[i][j][q], lse2);
+      const int at = out ? -1 : rows.at[i] - first;
+      if (__ballot(at >= 0 && at < FN * 16)) {  // of a row's columns few waves hold the target
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            if (held_column(lane, j, q) == at) acc[i][j][q] -= rows.d[i];
+      }
+    }
+    if (left < FN * 16) {
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            if (held_column(lane, j, q) >= left) acc[i][j][q] = 0.0f;
     }
   }
   __device__ inline int64_t columns(const ProductArgs&) const { return padded; }

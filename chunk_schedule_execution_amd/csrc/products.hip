@@ -18,28 +18,40 @@ int launch_rows(int dtype, const ProductArgs& g, const ProductPlan& plan, hipStr
 namespace {
 
 // ---- operands off the 16-byte grid ------------------------------------------------------
-// One pass over the operand, 5 us for the 1111 x 1001 of an odd product. Both operands in one
-// launch.
-
+// One pass over the operand, a vector per thread: written on the grid, read wherever it lies.
+// Short rows share a workgroup. 515 and 10007 rows of 333 fp32: 10.4 us with an element per
+// thread and a row per workgroup. Both operands in one launch.
 template <typename T>
 __global__ __launch_bounds__(256) void regrid_kernel(Regrid first, Regrid second) {
+  constexpr int V = 16 / int(sizeof(T));
+  typedef T wide __attribute__((ext_vector_type(V)));
+  typedef T wide_anywhere __attribute__((ext_vector_type(V), aligned(sizeof(T))));
   const Regrid g = blockIdx.z ? second : first;
-  const T* src = static_cast<const T*>(g.src);
-  T* dst = static_cast<T*>(g.dst);
-  const int64_t c = int64_t(blockIdx.y) * 1024 + threadIdx.x;
-  for (int64_t r = blockIdx.x; r < g.rows; r += gridDim.x)
+  const int64_t at = (int64_t(blockIdx.y) * blockDim.x + threadIdx.x) * V;
+  if (at >= g.ld_dst) return;
+  const int n = int(max(int64_t(0), min(int64_t(V), g.len - at)));
+  for (int64_t r = int64_t(blockIdx.x) * blockDim.y + threadIdx.y; r < g.rows; r += int64_t(gridDim.x) * blockDim.y) {
+    const T* src = static_cast<const T*>(g.src) + r * g.ld + at;
+    wide v;
+    if (n == V) {
+      v = *reinterpret_cast<const wide_anywhere*>(src);
+    } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t at = c + i * 256;
-      if (at < g.ld_dst) dst[r * g.ld_dst + at] = at < g.len ? src[r * g.ld + at] : T(0.0f);
+      for (int q = 0; q < V; ++q) v[q] = q < n ? src[q] : T(0.0f);
     }
+    *reinterpret_cast<wide*>(static_cast<T*>(g.dst) + r * g.ld_dst + at) = v;
+  }
 }
 
 int regrid(int dtype, const Regrid& first, const Regrid& second, hipStream_t s, std::string* err) {
-  const dim3 grid(unsigned(std::min<int64_t>(std::max(first.rows, second.rows), 1 << 20)),
-                  unsigned((std::max(first.ld_dst, second.ld_dst) + 1023) / 1024), second.rows ? 2 : 1);
-  if (dtype == CCL_BF16) hipLaunchKernelGGL(regrid_kernel<bf16>, grid, dim3(256), 0, s, first, second);
-  else hipLaunchKernelGGL(regrid_kernel<float>, grid, dim3(256), 0, s, first, second);
+  const int64_t vectors = std::max(first.ld_dst, second.ld_dst) / (dtype == CCL_BF16 ? 8 : 4);
+  int along = 16;
+  while (along < 256 && along < vectors) along *= 2;
+  const dim3 block(along, 256 / along);
+  const int64_t rows = (std::max(first.rows, second.rows) + block.y - 1) / block.y;
+  const dim3 grid(unsigned(std::min<int64_t>(rows, 1 << 20)), unsigned((vectors + along - 1) / along), second.rows ? 2 : 1);
+  if (dtype == CCL_BF16) hipLaunchKernelGGL(regrid_kernel<bf16>, grid, block, 0, s, first, second);
+  else hipLaunchKernelGGL(regrid_kernel<float>, grid, block, 0, s, first, second);
   return hip_status("regrid launch", err);
 }
 

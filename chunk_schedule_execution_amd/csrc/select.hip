@@ -89,6 +89,7 @@ __device__ inline V nan_first(V v) {
 template <typename V>
 __device__ inline int groups_before(const V* best, int groups, int g) {
   int before = 0;
+#pragma unroll 4
   for (int h = 0; h < groups; ++h) before += best[h] > best[g] || (best[h] == best[g] && h < g);
   return before;
 }
@@ -171,19 +172,18 @@ __device__ inline void choose_whole(const SelectArgs& a, int64_t t, WholeSpace<N
 }
 
 // ---- gates -----------------------------------------------------------------------------------
-// Of the chosen logits, read again (they are in the caches). x, top: the row, its maximum.
-template <typename T, int L, int Each, int NE>
+// x, top: the row and its maximum; logit(e): one of the row's by its number.
+template <int L, int Each, int NE, typename F>
 __device__ inline void write_gates(const SelectArgs& a, int64_t t, int lane, const int* chosen, const float (&x)[NE],
-                                   float top) {
+                                   float top, F logit) {
   const bool soft = a.score == CCL_SCORE_SOFTMAX;
-  const T* row = static_cast<const T*>(a.logits) + t * a.ld;
   int id[Each];
   float q[Each], m = kClosed, total = 1.0f;
 #pragma unroll
   for (int j = 0; j < Each; ++j) {
     const int c = j * L + lane;
     id[j] = c < a.choices && t < a.tokens ? chosen[c] : -1;
-    q[j] = id[j] >= 0 ? widen(row[id[j]]) : kClosed;
+    q[j] = id[j] >= 0 ? logit(id[j]) : kClosed;
     m = fmaxf(m, q[j]);
   }
   if (a.renorm) m = shared_top(over_max<L>(m), soft);
@@ -219,8 +219,9 @@ __global__ __launch_bounds__(kThreads) void select_whole_kernel(SelectArgs a) {
   if (t >= a.tokens) return;  // a whole wave
   choose_whole<T, NE>(a, t, space[wave], chosen[wave]);
   float x[NE];
-  load_row<64, 1>(static_cast<const T*>(a.logits) + t * a.ld, lane, a.experts, kClosed, x);
-  write_gates<T, 64, 1>(a, t, lane, chosen[wave], x, row_top<64>(x));
+  const T* row = static_cast<const T*>(a.logits) + t * a.ld;
+  load_row<64, 1>(row, lane, a.experts, kClosed, x);
+  write_gates<64, 1>(a, t, lane, chosen[wave], x, row_top<64>(x), [&](int e) { return widen(row[e]); });
 }
 
 // ---- 16 lanes for a token ----------------------------------------------------------------------
@@ -240,36 +241,38 @@ struct FewSpace {
   int expert[4][kCandidates];
   union {
     struct {
-      float value[4][kRow];
+      float row[4][kRow];  // the experts' values, while groups are ranked; then their logits
       float best[4][kFewGroups];
-    } groups;
+    } few;
     WholeSpace<(NE + 3) / 4> whole;
   };
   static __device__ inline int at(int e) { return e + (e >> 5) * 4; }
 };
 
-// What a value in fp32 may be off by, but for the addition of its bias (2^-24 of the sum). The
-// exponential's argument: p |x| 2^-24 with p |x| < 0.4; a step or two of p for the functions;
-// in a softmax, one for each of the sum's 20 additions.
-__device__ inline float value_off(bool soft) { return soft ? 0x1p-19f : 0x1p-21f; }
+// What a value in fp32 may be off by, but for the addition of its bias (2^-24 of the sum). In a
+// sigmoid p: p (1 - p) (2 + |x|) 2^-24 by the exponential and its argument, below 2^-24, and 3
+// times 2^-24 p by the sum and the reciprocal. In a softmax: p |x| 2^-24 with p |x| < 0.4 by the
+// argument, and 2^-24 p for each of the sum's 20 additions and for the functions.
+__device__ inline float value_off(bool soft) { return soft ? 0x1p-19f : 0x1p-22f; }
 
 // Takes the keys of experts outside the kept groups away; true where fp32 cannot tell which
 // those are. v: the experts' values, exact where they are the logits.
 template <bool Scored, int V, int NE>
 __device__ inline bool keep_groups(const SelectArgs& a, FewSpace<NE>& space, int token, int lane, const float (&v)[NE],
                                    float (&key)[NE]) {
-  auto& s = space.groups;
+  auto& s = space.few;
   const int groups = a.groups, parts = 1 << a.parts_log2;
 #pragma unroll
-  for (int i = 0; i < NE; ++i) s.value[token][space.at(expert_at<16, V>(i, lane))] = v[i];
+  for (int i = 0; i < NE; ++i) s.row[token][space.at(expert_at<16, V>(i, lane))] = v[i];
   __builtin_amdgcn_wave_barrier();
   // the lanes share out the groups, or parts of a group where those are few
+  float size = 0.0f;  // of the values that groups' values are made of
   for (int j = lane; j < groups * parts; j += 16) {
     const int g = j >> a.parts_log2, end = g * a.per + a.per;
     float first = kClosed, second = kClosed;
 #pragma unroll 4
     for (int e = g * a.per + (j & (parts - 1)); e < end; e += parts) {
-      const float w = s.value[token][space.at(e)];
+      const float w = s.row[token][space.at(e)];
       second = fmaxf(second, fminf(first, w));
       first = fmaxf(first, w);
     }
@@ -278,7 +281,9 @@ __device__ inline bool keep_groups(const SelectArgs& a, FewSpace<NE>& space, int
       second = fmaxf(fmaxf(second, u), fminf(first, w));
       first = fmaxf(first, w);
     }
-    s.best[token][g] = a.best == 2 && second > kClosed ? first + second : first;
+    const bool two = a.best == 2 && second > kClosed;
+    s.best[token][g] = two ? first + second : first;
+    if (Scored && first > kClosed) size = fmaxf(size, fabsf(first) + (two ? fabsf(second) : 0.0f));
   }
   __builtin_amdgcn_wave_barrier();
   float lowest = INFINITY, highest = kClosed;  // of the groups that stay, of the others
@@ -305,8 +310,9 @@ __device__ inline bool keep_groups(const SelectArgs& a, FewSpace<NE>& space, int
   if (!Scored) return false;
   lowest = -over_max<16>(-lowest);
   highest = over_max<16>(highest);
-  // sums of two values on either side
-  return highest > kClosed && !(lowest - highest > 4 * value_off(a.score == CCL_SCORE_SOFTMAX) + 0x1p-21f * fabsf(highest));
+  size = over_max<16>(size);
+  // on either side two values and their sum: 2 offs, and 2^-24 of the size for each addition
+  return highest > kClosed && !(lowest - highest > 4 * value_off(a.score == CCL_SCORE_SOFTMAX) + 0x1p-22f * size);
 }
 
 // Scored: experts are ranked by p + bias, or groups by sums of p. Otherwise by their logits,
@@ -382,6 +388,10 @@ __global__ __launch_bounds__(kThreads) void select_kernel(SelectArgs a) {
     }
   }
 
+  // (a wave's LDS accesses are in order: nothing of the groups is overwritten before it is read)
+#pragma unroll
+  for (int i = 0; i < NE; ++i) space.few.row[token][space.at(expert_at<16, V>(i, lane))] = x[i];
+
   // the choices-th highest of the lanes' maxima: at least `choices` experts reach it
   float most = key[0];
 #pragma unroll
@@ -418,7 +428,7 @@ __global__ __launch_bounds__(kThreads) void select_kernel(SelectArgs a) {
   __builtin_amdgcn_wave_barrier();
   for (int c = lane; c < count; c += 16) {
     const int e = space.expert[token][c];
-    const float logit = widen(row[e]);
+    const float logit = space.few.row[token][space.at(e)];
     space.value[token][c] =
         nan_first(Scored && a.bias ? score_of(logit, top, total, soft) + double(a.bias[e]) : double(logit));
   }
@@ -427,6 +437,7 @@ __global__ __launch_bounds__(kThreads) void select_kernel(SelectArgs a) {
     const double v = space.value[token][c];
     const int e = space.expert[token][c];
     int rank = 0;
+#pragma unroll 4
     for (int d = 0; d < count; ++d) {
       const double w = space.value[token][d];
       rank += w > v || (w == v && space.expert[token][d] < e);
@@ -436,7 +447,7 @@ __global__ __launch_bounds__(kThreads) void select_kernel(SelectArgs a) {
   __builtin_amdgcn_wave_barrier();
 
   const unsigned long long doubts = __ballot(doubt && t < a.tokens);
-  if (doubts) {
+  if (doubts) {  // takes the place of the logits in LDS
 #pragma nounroll
     for (int j = 0; j < 4; ++j) {
       if (!((doubts >> (j * 16)) & 0xffff)) continue;
@@ -444,8 +455,12 @@ __global__ __launch_bounds__(kThreads) void select_kernel(SelectArgs a) {
       if (token == j && lane < a.choices) space.chosen[j][lane] = space.whole_chosen[lane];
       __builtin_amdgcn_wave_barrier();
     }
+#pragma unroll
+    for (int i = 0; i < NE; ++i) space.few.row[token][space.at(expert_at<16, V>(i, lane))] = x[i];
+    __builtin_amdgcn_wave_barrier();
   }
-  write_gates<T, 16, 1>(a, t, lane, space.chosen[token], x, top);
+  write_gates<16, 1>(a, t, lane, space.chosen[token], x, top,
+                     [&](int e) { return space.few.row[token][space.at(e)]; });
 }
 
 // ---- the gradient --------------------------------------------------------------------------
