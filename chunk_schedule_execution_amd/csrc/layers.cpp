@@ -111,7 +111,7 @@ struct LossPlan {
   int64_t at_dz = 0, at_dx = 0, at_product = 0, ld_dz = 0;   // backward
   int64_t piece = 0;
   bool onto = false;  // dx is summed up over the pieces
-  ProductPlan dx;
+  ProductPlan logits, dx;
   int64_t total = 0;
 };
 
@@ -150,11 +150,40 @@ ProductPlan dw_plan(const ccl_cross_entropy_desc& d, const LossPlan& p, int64_t 
   return plan_product(d.dtype, true, true, kPlain, dw_args(d, p, columns), kPadded, kPadded);
 }
 
+// Of a piece of the backward pass, whose operands lie on the grid.
+ProductPlan logits_plan(const ccl_cross_entropy_desc& d, const LossPlan& p, int64_t columns) {
+  return plan_product(d.dtype, false, false, kPlain, logits_args(d, p, columns), kPadded, kPadded);
+}
+
+// Whether a product's logits go through the workspace instead of staying in registers: where
+// it has few rows and a kernel without tiles (3 x 1190 x 11136 fp32: 50 us in tiles, whose
+// operands have to be copied first), and where its tiles are fewer than the compute units and
+// its sums are split, or most units would idle (113 x 1984 x 4562 fp32: 41 us unsplit). Both
+// come for logits that are small beside the operands. With tiles for all units the split no
+// longer pays (64 x 4096 x 32768 bf16: 57 us unsplit, 65 in 2 splits).
+bool through_memory(const ProductPlan& p, const ProductArgs& g) {
+  return p.kind == kRows16 || (p.splits > 1 && ((g.m + 63) / 64) * ((g.n + 63) / 64) < 256);
+}
+int64_t logits_bytes(const ProductPlan& p, const ProductArgs& g) {
+  return p.at_partial + p.splits * g.m * partial_ld(g.n) * 4;
+}
+
 LossPlan loss_plan(const ccl_cross_entropy_desc& d, bool backward) {
   LossPlan p;
   const int64_t size = elem_size(d.dtype), v = 16 / size;
   auto up = [&](int64_t n) { return (n + v - 1) / v * v; };
   const bool off = d.flags & CCL_LINEAR_UNALIGNED;
+  if (!backward) {
+    p.ld_x = d.ld_x;
+    p.ld_w = d.ld_w;
+    const OperandGrid grid = off ? kOffGrid : kByStrides;
+    const ProductArgs g = logits_args(d, p, d.vocabulary);
+    p.logits = plan_product(d.dtype, false, false, kPlain, g, grid, grid);
+    if (through_memory(p.logits, g)) {
+      p.total = align16(logits_bytes(p.logits, g));
+      return p;
+    }
+  }
   p.copy_x = off || d.ld_x % v || d.in_features % v;
   p.copy_w = off || d.ld_w % v || d.in_features % v;
   p.ld_x = p.copy_x ? up(d.in_features) : d.ld_x;
@@ -176,8 +205,12 @@ LossPlan loss_plan(const ccl_cross_entropy_desc& d, bool backward) {
   p.at_dx = p.at_dz + align16(d.rows * p.ld_dz * size);
   p.at_product = p.at_dx + (p.onto ? p.dx.splits * d.rows * partial_ld(d.in_features) * 4 : 0);
   int64_t most = p.onto ? 0 : p.dx.bytes;
-  for (int64_t lo = 0; lo < d.vocabulary; lo += p.piece)
-    most = std::max(most, dw_plan(d, p, std::min(p.piece, d.vocabulary - lo)).bytes);
+  for (int64_t lo = 0; lo < d.vocabulary; lo += p.piece) {
+    const int64_t n = std::min(p.piece, d.vocabulary - lo);
+    most = std::max(most, dw_plan(d, p, n).bytes);
+    const ProductPlan logits = logits_plan(d, p, n);
+    if (through_memory(logits, logits_args(d, p, n))) most = std::max(most, logits_bytes(logits, logits_args(d, p, n)));
+  }
   p.total = p.at_product + most;
   return p;
 }
@@ -222,15 +255,31 @@ int loss_forward(const ccl_cross_entropy_desc* desc, const void* x, const void* 
   const LossPlan p = loss_plan(d, false);
   check_workspace(ws, ws_bytes, p.total);
   unsigned char* const space = static_cast<unsigned char*>(ws);
-  operands(d, p, space, stream, &x, &w);
+  std::string err;
   ProductArgs g = logits_args(d, p, d.vocabulary);
+  LossArgs l = loss_args(d, targets);
+  if (through_memory(p.logits, g)) {
+    g.a = x;
+    g.b = w;
+    g.partial = reinterpret_cast<float*>(space + p.logits.at_partial);
+    launched(launch_product_sums(d.dtype, false, false, kPlain, g, p.logits, space, stream, &err), err);
+    LossRowsArgs r;
+    r.partial = g.partial;
+    r.rows = d.rows;
+    r.n = d.vocabulary;
+    r.splits = p.logits.splits;
+    r.loss_out = loss;
+    r.lse_out = lse;
+    l.picked = picked;
+    launched(launch_loss_rows(r, l, stream, &err), err);
+    return CCL_OK;
+  }
+  operands(d, p, space, stream, &x, &w);
   const ProductKind kind = unsplit_tile(d.dtype, g);
   g.a = x;
   g.b = w;
-  LossArgs l = loss_args(d, targets);
   l.sums = reinterpret_cast<float*>(space + p.at_sums);
   l.picked = picked ? picked : reinterpret_cast<float*>(space + p.at_picked);
-  std::string err;
   launched(launch_loss_sums(d.dtype, g, l, kind, stream, &err), err);
   LossJoinArgs j;
   j.pairs = l.sums;
@@ -282,7 +331,21 @@ int loss_backward(const ccl_cross_entropy_desc* desc, const float* dloss, const 
       g.c = space + p.at_dz;
       g.ldc = p.ld_dz;
       l.first = int(first + lo);
-      launched(launch_loss_slope(d.dtype, g, l, (n + v - 1) / v * v, unsplit_tile(d.dtype, g), stream, &err), err);
+      const ProductPlan logits = logits_plan(d, p, n);
+      if (through_memory(logits, g)) {
+        g.partial = reinterpret_cast<float*>(space + p.at_product + logits.at_partial);
+        launched(launch_product_sums(d.dtype, false, false, kPlain, g, logits, space + p.at_product, stream, &err), err);
+        LossRowsArgs r;
+        r.partial = g.partial;
+        r.rows = d.rows;
+        r.n = n;
+        r.splits = logits.splits;
+        r.dz = space + p.at_dz;
+        r.ldz = p.ld_dz;
+        launched(launch_loss_rows_slope(d.dtype, r, l, stream, &err), err);
+      } else {
+        launched(launch_loss_slope(d.dtype, g, l, (n + v - 1) / v * v, unsplit_tile(d.dtype, g), stream, &err), err);
+      }
     }
     if (dx && d.rows > 0) {
       ProductArgs g = dx_args(d, p, n);

@@ -74,6 +74,17 @@ int launch_loss_sums(int dtype, const ProductArgs& g, const LossArgs& loss, Prod
 // g.n up to `padded`.
 int launch_loss_slope(int dtype, const ProductArgs& g, const LossArgs& loss, int64_t padded, ProductKind kind,
                       void* stream, std::string* err);
+// The same two from the fp32 sums of `splits` splits of a product in g.partial.
+struct LossRowsArgs {
+  const float* partial = nullptr;
+  int64_t rows = 0, n = 0, ldz = 0;  // ldz: dz's
+  int splits = 1;
+  float* loss_out = nullptr;         // NULL: not wanted
+  float* lse_out = nullptr;
+  void* dz = nullptr;
+};
+int launch_loss_rows(const LossRowsArgs& args, const LossArgs& loss, void* stream, std::string* err);
+int launch_loss_rows_slope(int dtype, const LossRowsArgs& args, const LossArgs& loss, void* stream, std::string* err);
 // A b_by_k product whose sums are written to g.partial (fresh) or added to what is there.
 int launch_product_onto(int dtype, const ProductArgs& g, const ProductPlan& plan, bool fresh, void* stream,
                         std::string* err);

@@ -9,9 +9,10 @@ namespace prod {
 namespace {
 
 // 16 bytes of a row from element k on, zeros from k_end on. Vec: rows on the 16-byte grid
-// and k_end a multiple of the vector.
+// and k_end a multiple of the vector. `whole`: the row has a vector's values at least (of
+// those, `k_end` says how many count here).
 template <typename T, bool Vec>
-__device__ inline auto load_k(const T* row, int k, int k_end) {
+__device__ inline auto load_k(const T* row, int k, int k_end, bool whole) {
   constexpr int V = 16 / int(sizeof(T));
   typedef T vec __attribute__((ext_vector_type(V)));
   vec v;
@@ -20,6 +21,13 @@ __device__ inline auto load_k(const T* row, int k, int k_end) {
     v = *reinterpret_cast<const vec*>(row + (k < k_end ? k : 0));
     const vec zero = {};
     v = k < k_end ? v : zero;
+  } else if (whole) {
+    // off the grid, whole vectors all the same; one that would cross the row's end is read
+    // from further ahead and moved down
+    typedef T anywhere __attribute__((ext_vector_type(V), aligned(sizeof(T))));
+    const int at = max(0, min(k, k_end - V)), late = k - at;
+    const unsigned __int128 bits = __builtin_bit_cast(unsigned __int128, *reinterpret_cast<const anywhere*>(row + at));
+    v = __builtin_bit_cast(vec, late < V ? bits >> (late * 8 * int(sizeof(T))) : (unsigned __int128)0);
   } else {
 #pragma unroll
     for (int q = 0; q < V; ++q) {
@@ -60,7 +68,8 @@ __device__ inline void product_rows(const ProductArgs& g, int slabs) {
 #pragma unroll
     for (int j = 0; j < FN; ++j) cols[j] = B + min(col + j * 16 + (lane & 15), g.n - 1) * g.ldb;
     const int part = (lane >> 4) * V;
-    typedef decltype(load_k<T, Vec>(A, 0, 0)) vec;
+    typedef decltype(load_k<T, Vec>(A, 0, 0, true)) vec;
+    const bool whole = g.k >= V;
     for (int l0 = first + wave; l0 < last; l0 += 4 * Deep) {
       vec a[Deep][2], b[Deep][2][FN];
 #pragma unroll
@@ -69,8 +78,8 @@ __device__ inline void product_rows(const ProductArgs& g, int slabs) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
 #pragma unroll
-          for (int j = 0; j < FN; ++j) b[d][h][j] = load_k<T, Vec>(cols[j], k + h * 4 * V, end);
-          a[d][h] = load_k<T, Vec>(row, k + h * 4 * V, end);
+          for (int j = 0; j < FN; ++j) b[d][h][j] = load_k<T, Vec>(cols[j], k + h * 4 * V, end, whole);
+          a[d][h] = load_k<T, Vec>(row, k + h * 4 * V, end, whole);
         }
       }
       __builtin_amdgcn_sched_barrier(0);  // loads stay ahead of all products

@@ -58,6 +58,10 @@ ProductPlan plan_product(int dtype, bool a_by_k, bool b_by_k, ProductMode mode, 
 int64_t rows16_workgroups(ProductMode mode, const ProductArgs& args, int columns);
 int launch_product(int dtype, bool a_by_k, bool b_by_k, ProductMode mode, const ProductArgs& args,
                    const ProductPlan& plan, void* workspace, void* stream, std::string* err);
+// The same without the splits' sum: args.partial holds them afterwards (or is NULL, where
+// there is one split). The workspace is used up to plan.at_partial.
+int launch_product_sums(int dtype, bool a_by_k, bool b_by_k, ProductMode mode, const ProductArgs& args,
+                        const ProductPlan& plan, void* workspace, void* stream, std::string* err);
 
 // The tile that a product of these sizes takes when its sums are not split.
 ProductKind unsplit_tile(int dtype, const ProductArgs& args);

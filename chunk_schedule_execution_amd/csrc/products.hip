@@ -324,8 +324,8 @@ int launch_join(int dtype, const ProductArgs& args, int splits, void* stream, st
   return prod::join(dtype, args, splits, reinterpret_cast<hipStream_t>(stream), err);
 }
 
-int launch_product(int dtype, bool a_by_k, bool b_by_k, ProductMode mode, const ProductArgs& args,
-                   const ProductPlan& plan, void* workspace, void* stream, std::string* err) {
+int launch_product_sums(int dtype, bool a_by_k, bool b_by_k, ProductMode mode, const ProductArgs& args,
+                        const ProductPlan& plan, void* workspace, void* stream, std::string* err) {
   using namespace prod;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   ProductArgs g = args;
@@ -348,13 +348,18 @@ int launch_product(int dtype, bool a_by_k, bool b_by_k, ProductMode mode, const 
   // (no rows: the gradient of no rows, whose products are empty sums)
   if (copies && std::max(copy[0].rows, copy[1].rows) > 0)
     if (int rc = regrid(dtype, copy[0], copy[1], s, err)) return rc;
-  if (plan.splits > 1) g.partial = reinterpret_cast<float*>(ws + plan.at_partial);
-  int rc;
-  if (plan.kind == kRows16) rc = launch_rows(dtype, g, plan, s, err);
-  else if (dtype == CCL_BF16) rc = launch_tile_bf16(a_by_k, b_by_k, mode, g, plan, s, err);
-  else rc = launch_tile_f32(a_by_k, b_by_k, mode, g, plan, s, err);
+  if (plan.kind == kRows16) return launch_rows(dtype, g, plan, s, err);
+  if (dtype == CCL_BF16) return launch_tile_bf16(a_by_k, b_by_k, mode, g, plan, s, err);
+  return launch_tile_f32(a_by_k, b_by_k, mode, g, plan, s, err);
+}
+
+int launch_product(int dtype, bool a_by_k, bool b_by_k, ProductMode mode, const ProductArgs& args,
+                   const ProductPlan& plan, void* workspace, void* stream, std::string* err) {
+  ProductArgs g = args;
+  if (plan.splits > 1) g.partial = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + plan.at_partial);
+  const int rc = launch_product_sums(dtype, a_by_k, b_by_k, mode, g, plan, workspace, stream, err);
   if (rc || plan.splits == 1) return rc;
-  return join(dtype, g, plan.splits, s, err);
+  return prod::join(dtype, g, plan.splits, reinterpret_cast<hipStream_t>(stream), err);
 }
 
 }  // namespace ccl

@@ -14,7 +14,8 @@ pytestmark = pytest.mark.gpu
 # 16-byte grid, each tile
 SHAPES = [(1, 1, 1), (1, 8, 2), (2, 7, 5), (3, 64, 40), (1, 512, 1000), (16, 33, 130), (17, 100, 33), (63, 257, 65),
           (64, 128, 128), (65, 72, 257), (100, 1000, 48), (130, 72, 300), (255, 192, 513), (300, 264, 1031),
-          (520, 136, 2050), (257, 320, 4096), (1000, 40, 3001), (2100, 64, 2600), (40, 128, 20000), (2048, 512, 6144)]
+          (520, 136, 2050), (257, 320, 4096), (3, 1190, 11136), (15, 810, 683), (16, 2048, 5003), (40, 4096, 77),
+          (64, 831, 7552), (300, 4096, 1000), (500, 2050, 9), (1000, 40, 3001), (2100, 64, 2600), (40, 128, 20000), (2048, 512, 6144)]
 
 
 def inputs(seed, rows, k, vocabulary, dtype, shard=None, pad=0, total=None):

@@ -197,9 +197,10 @@ def test_cross_entropy_workspace_of_every_size(rows, dtype):
         forward, backward = (capi.ccl_linear_cross_entropy_workspace(d, b) for b in (False, True))
         assert forward >= 0 and backward >= 0
         if k % 8 == 0:
-            assert forward <= rows * ((v + 31) // 32 * 8 + 8) + 64
+            # a pair for 32 logits; small products' sums go through memory
+            assert forward <= max(rows * ((v + 31) // 32 * 8 + 8) + 64, 256 << 20)
             dz = rows * max(8192 + 256, (512 << 20) // max(1, rows * size) + 256) * size
-            assert backward <= dz + 17 * (rows + v) * (k + 16) * 4 + 4096
+            assert backward <= dz + 17 * (rows + v) * (k + 16) * 4 + (256 << 20)
 
 
 def test_join_refuses_bad_arguments():
