@@ -56,21 +56,21 @@ int regrid(int dtype, const Regrid& first, const Regrid& second, hipStream_t s, 
 }
 
 // ---- joining the splits of the summed dimension -------------------------------------------
-// A workgroup takes 16 rows of a group by 256 columns, 8 columns per thread, and adds the
-// splits in order.
-constexpr int kJoinRows = 16;
-
-template <typename T>
-__global__ __launch_bounds__(256) void join_kernel(ProductArgs g, int splits) {
-  const RowTile t = find_tile(g.offsets, g.groups, g.m, kJoinRows, blockIdx.x);
+// A workgroup takes rows of a group by 256 columns, 8 columns per thread, and adds the splits
+// in order. 16 rows where those are workgroups enough; otherwise one wave for 2 rows (16
+// splits of 64 x 4096: 8.0 us in sixteens).
+template <typename T, int Rows>
+__global__ __launch_bounds__(Rows >= 16 ? 256 : 64) void join_kernel(ProductArgs g, int splits) {
+  constexpr int Pass = Rows >= 16 ? 8 : 2;  // rows at a time
+  const RowTile t = find_tile(g.offsets, g.groups, g.m, Rows, blockIdx.x);
   const int64_t c = int64_t(blockIdx.y) * 256 + (threadIdx.x & 31) * 8;
   if (t.group < 0 || c >= g.n) return;
   const bool nothing = g.offsets && t.group == g.groups;
-  const int64_t end = min(t.end, t.row + kJoinRows);
+  const int64_t end = min(t.end, t.row + Rows);
   const int n = int(min(int64_t(8), g.n - c));
   const int64_t first = t.row + (threadIdx.x >> 5);
-  Finish<T> finish(g, static_cast<T*>(g.c), first, 8, c, n, t.group, nothing);
-  for (int64_t r = first; r < end; r += 8) {
+  Finish<T> finish(g, static_cast<T*>(g.c), first, Pass, c, n, t.group, nothing);
+  for (int64_t r = first; r < end; r += Pass) {
     float z[8] = {};
     if (!nothing) {
 #pragma unroll 4
@@ -86,10 +86,17 @@ __global__ __launch_bounds__(256) void join_kernel(ProductArgs g, int splits) {
   }
 }
 
+template <typename T>
+void join_t(const ProductArgs& g, int splits, hipStream_t s) {
+  const int64_t columns = (g.n + 255) / 256, groups = g.offsets ? g.groups : 0;
+  auto grid = [&](int rows) { return dim3(unsigned((g.m + rows - 1) / rows + groups), unsigned(columns)); };
+  if ((g.m + 15) / 16 * columns >= 512) hipLaunchKernelGGL((join_kernel<T, 16>), grid(16), dim3(256), 0, s, g, splits);
+  else hipLaunchKernelGGL((join_kernel<T, 2>), grid(2), dim3(64), 0, s, g, splits);
+}
+
 int join(int dtype, const ProductArgs& g, int splits, hipStream_t s, std::string* err) {
-  const dim3 grid(unsigned((g.m + kJoinRows - 1) / kJoinRows + (g.offsets ? g.groups : 0)), unsigned((g.n + 255) / 256));
-  if (dtype == CCL_BF16) hipLaunchKernelGGL(join_kernel<bf16>, grid, dim3(256), 0, s, g, splits);
-  else hipLaunchKernelGGL(join_kernel<float>, grid, dim3(256), 0, s, g, splits);
+  if (dtype == CCL_BF16) join_t<bf16>(g, splits, s);
+  else join_t<float>(g, splits, s);
   return hip_status("join launch", err);
 }
 
