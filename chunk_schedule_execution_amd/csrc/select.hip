@@ -294,18 +294,19 @@ __device__ inline bool keep_groups(const SelectArgs& a, FewSpace<NE>& space, int
     else if (g < groups) highest = fmaxf(highest, s.best[token][g]);
     kept |= (unsigned(__ballot(stays) >> (token * 16)) & 0xffff) << (g & 16);
   }
-  // (past the last expert keys are closed already)
+  // past the last expert keys are closed already, whatever their group would be
+  auto stays = [&](int i) { return kept >> (group_of(expert_at<16, V>(i, lane), a.magic) & 31) & 1; };
   if (V > 1 && a.per % V == 0) {  // whole vectors
 #pragma unroll
     for (int i = 0; i < NE; i += V) {
-      const bool out = !(kept >> group_of(expert_at<16, V>(i, lane), a.magic) & 1);
+      const bool out = !stays(i);
 #pragma unroll
       for (int q = 0; q < V; ++q) key[i + q] = out ? kClosed : key[i + q];
     }
   } else {
 #pragma unroll
     for (int i = 0; i < NE; ++i)
-      if (!(kept >> group_of(expert_at<16, V>(i, lane), a.magic) & 1)) key[i] = kClosed;
+      if (!stays(i)) key[i] = kClosed;
   }
   if (!Scored) return false;
   lowest = -over_max<16>(-lowest);

@@ -90,6 +90,41 @@ def test_select_compares_in_64_bits(score):
     check(x * 1e-6, 6, score=score, groups=8, kept_groups=3, group_best=2)
 
 
+def ids_in_order(logits, choices, score, bias, groups, kept, best):
+    """Many tokens at once: stable sorts of the 64-bit values."""
+    x = logits.double()
+    t, e = x.shape
+    value = L.scores(x, score) + (0.0 if bias is None else bias.double())
+    value = value.masked_fill(x == -INF, -INF)
+    order = value if bias is not None else x
+    if kept < groups:
+        top = value.view(t, groups, -1).sort(2, descending=True).values[:, :, :best]
+        total = top.masked_fill(top == -INF, 0.0).sum(2).masked_fill(top[:, :, 0] == -INF, -INF)
+        stay = torch.sort(total, dim=1, descending=True, stable=True).indices[:, :kept]
+        mask = torch.zeros(t, groups, dtype=torch.bool, device=x.device).scatter_(1, stay, True)
+        order = order.masked_fill(~mask.repeat_interleave(e // groups, 1), -INF)
+    values, ids = torch.sort(order, dim=1, descending=True, stable=True)
+    return ids.masked_fill(values == -INF, -1)[:, :choices].to(torch.int32)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("experts,choices,groups,kept,best", [
+    (256, 8, 8, 4, 2), (256, 8, 1, 1, 1), (128, 12, 16, 3, 1), (64, 4, 4, 2, 2), (61, 3, 1, 1, 1), (250, 10, 25, 6, 2),
+    (32, 2, 32, 20, 2), (192, 13, 6, 2, 2), (128, 4, 64, 5, 2)])
+def test_select_many_tokens(experts, choices, groups, kept, best, score):
+    """Enough tokens that some are close to a tie, in fp32 below what it resolves, and some have
+    more experts near the border than are looked at in 64 bits one by one."""
+    for dtype, rounded in (("f32", False), ("bf16", False), ("f32", True)):
+        logits = inputs(17, 20000, experts, dtype, 0.05)
+        if rounded:  # few different logits: ties everywhere
+            logits = logits.mul(2).round().div(2)
+        for bias in (None, normal(18, experts, scale=0.05), normal(19, experts).round() * 2.0 ** 20):
+            got, _ = ops.expert_select(logits, choices, score=score, bias=bias, groups=groups, kept_groups=kept,
+                                       group_best=best)
+            want = ids_in_order(logits, choices, score, bias, groups, kept, best)
+            assert torch.equal(got, want), (dtype, rounded, int((got != want).any(1).sum()))
+
+
 @pytest.mark.parametrize("lowest", [-100.0, -700.0, float(torch.finfo(torch.bfloat16).min)])
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 def test_select_of_masks_of_the_lowest_value(score, lowest):
