@@ -30,7 +30,7 @@ __device__ inline int held_column(int lane, int j, int q) { return j * 16 + (lan
 // Leaves per row the maximum of a wave's columns and the sum of exp(z - maximum): 8 bytes for
 // 64 logits. The maximum is the wave's own, so no wave waits for another.
 struct RowSums {
-  static constexpr bool kTakes = true, kAdds = false;
+  static constexpr bool kTakes = true, kAdds = false, kPlainStores = false;
   LossArgs loss;
 
   template <int FM>
@@ -98,7 +98,7 @@ struct RowSums {
 
 // Turns logits into their gradient, which is then written as a product's results are.
 struct LossSlope {
-  static constexpr bool kTakes = false, kAdds = false;
+  static constexpr bool kTakes = false, kAdds = false, kPlainStores = true;
   LossArgs loss;
   int64_t padded;
 

@@ -227,7 +227,7 @@ __device__ inline TileJob find_job(const ProductArgs& g, ProductMode mode, unsig
 
 // The usual end of a tile: bias, activation, residual and stores, or the splits' sums.
 struct Results {
-  static constexpr bool kTakes = false, kAdds = false;
+  static constexpr bool kTakes = false, kAdds = false, kPlainStores = false;
   template <int FM>
   struct Rows {
     __device__ inline void load(const Results&, const ProductArgs&, const TileJob&, int) {}
@@ -407,6 +407,8 @@ __device__ inline void product_tiles(const ProductArgs& g, const End& ending, Pr
           store8(sums, true, n, v);
         } else if (g.partial) {
           store8(partial_at(g, blockIdx.y, int64_t(job.row) + in, c), true, n, v);
+        } else if constexpr (End::kPlainStores) {
+          store8<false>(finish.out, finish.vec_c, n, v);
         } else {
           finish.row(v);
         }
