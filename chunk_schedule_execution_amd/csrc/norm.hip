@@ -108,8 +108,8 @@ __device__ inline void row_sums(float& v, float& w, float (*parts)[Sharing<R>::k
 
 // ---- forward -------------------------------------------------------------------------------
 // The variance is the mean of squared differences from the mean, from registers: nothing
-// cancels. 16384 x 4096 bf16 with residual and both outputs (537 MB): 106 us with one row per
-// wave and no walk.
+// cancels. 16384 x 4096 bf16 with residual and both outputs (537 MB): 95 us, 5.7 TB/s; 106 with
+// a wave to each row and no walk. A copy of 1 GB reaches 5.1.
 template <typename T, int Held, int R>
 __global__ __launch_bounds__(Sharing<R>::kThreads) void norm_kernel(NormArgs a) {
   using P = Pack<T>;
@@ -271,8 +271,8 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(NormArgs a) {
 // With g = dout w and y = (x - mean) rstd: dx = rstd (g - mean(g) - y mean(g y)) + dtotal,
 // dw = sum over the rows of dout y, db of dout. A thread keeps to its columns, whose share of dw
 // and db stays in registers: one pass over the rows gives all three, and each workgroup leaves
-// its share in `partial`. 16384 x 4096 bf16 with dtotal (537 MB): 94 us, 5.7 TB/s; 134 without
-// the next row's loads ahead.
+// its share in `partial`. 16384 x 4096 bf16 with dtotal (537 MB): 90 to 94 us, 5.7 TB/s; 134
+// without the next row's loads ahead.
 template <typename T, int Held, int R>
 __global__ __launch_bounds__(Sharing<R>::kThreads) void norm_backward_kernel(NormArgs a) {
   using P = Pack<T>;
@@ -510,7 +510,10 @@ __global__ __launch_bounds__(1024) void norm_sum_kernel(NormArgs a, int64_t shar
 
 // ---- choice of kernels -----------------------------------------------------------------------
 // Calls f with the threads to a row and the packs of each that hold a row of n packs; false
-// where none do. Eight only in fp32, where they are as many values as four in bf16.
+// where none do: there rows are read again instead (2048 x 16384 bf16 gradients, the widest in
+// registers, 86 us; 1024 x 20000, read again, 66 for 0.6 times the bytes). A wave a row needs no
+// barrier, but has all of the row's latency: only up to two packs a lane. Eight packs only in
+// fp32, where they are as many values as four in bf16.
 template <typename T, typename F>
 bool by_width(int64_t n, F f) {
   using std::integral_constant;
@@ -531,8 +534,7 @@ template <typename T>
 int64_t packs(int64_t width) {
   return (width * int64_t(sizeof(T)) + 15) / 16;
 }
-// Workgroups that walk `rows` rows, `side` of them side by side: no more than are resident,
-// and for the gradients no more than leave a share of dw and db worth adding up.
+// Workgroups that walk `rows` rows, `side` of them side by side, at most `most`.
 int64_t walkers(int64_t rows, int side, int64_t most) {
   return std::max<int64_t>(1, std::min<int64_t>(most, (rows + side - 1) / side));
 }
@@ -549,6 +551,10 @@ int norm_t(const NormArgs& a, hipStream_t s, std::string* err) {
   return hip_status("layer norm launch", err);
 }
 
+// Workgroups of the gradients: as many as are resident (half of 512 threads: 4096 x 8192 bf16
+// takes 64 us in 256 shares and 76 in 512), and each with four rows at least, or the shares of dw
+// and db would be as much to write and add up as the rows (1111 x 4096 bf16: 19 us, 28 with a
+// workgroup a row).
 constexpr int64_t kMostShares = 512, kRowsEach = 4;
 int64_t band_height(int64_t rows) { return std::max<int64_t>(64, (rows + kMostShares - 1) / kMostShares); }
 
