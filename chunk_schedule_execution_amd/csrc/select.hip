@@ -250,6 +250,7 @@ struct FewSpace {
     WholeSpace<(NE + 3) / 4> whole;
   };
   static __device__ inline int at(int e) { return e + (e >> 5) * 4; }
+  static __device__ inline int at_pair(int p) { return 2 * (p + (p >> 3)); }
 };
 
 // What a value in fp32 may be off by, but for the addition of its bias (2^-24 of the sum). In a
@@ -265,19 +266,45 @@ __device__ inline bool keep_groups(const SelectArgs& a, FewSpace<NE>& space, int
                                    float (&key)[NE]) {
   auto& s = space.few;
   const int groups = a.groups, parts = 1 << a.parts_log2;
+  const bool vectors = V > 1 && a.per % V == 0;  // no vector lies in two groups
+  if (vectors) {
+    // the two best of a vector, from registers
 #pragma unroll
-  for (int i = 0; i < NE; ++i) s.row[token][space.at(expert_at<16, V>(i, lane))] = v[i];
+    for (int i = 0; i < NE; i += V) {
+      float first = fmaxf(v[i], v[i + 1]), second = fminf(v[i], v[i + 1]);
+#pragma unroll
+      for (int q = 2; q < V; q += 2) {
+        const float high = fmaxf(v[i + q], v[i + q + 1]), low = fminf(v[i + q], v[i + q + 1]);
+        second = fmaxf(fmaxf(second, low), fminf(first, high));
+        first = fmaxf(first, high);
+      }
+      *reinterpret_cast<float2*>(&s.row[token][space.at_pair(expert_at<16, V>(i, lane) / V)]) = make_float2(first, second);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NE; ++i) s.row[token][space.at(expert_at<16, V>(i, lane))] = v[i];
+  }
   __builtin_amdgcn_wave_barrier();
   // the lanes share out the groups, or parts of a group where those are few
   float size = 0.0f;  // of the values that groups' values are made of
   for (int j = lane; j < groups * parts; j += 16) {
-    const int g = j >> a.parts_log2, end = g * a.per + a.per;
+    const int g = j >> a.parts_log2, part = j & (parts - 1);
     float first = kClosed, second = kClosed;
+    if (vectors) {
+      const int per = a.per / V;
 #pragma unroll 4
-    for (int e = g * a.per + (j & (parts - 1)); e < end; e += parts) {
-      const float w = s.row[token][space.at(e)];
-      second = fmaxf(second, fminf(first, w));
-      first = fmaxf(first, w);
+      for (int e = g * per + part; e < g * per + per; e += parts) {
+        const float2 w = *reinterpret_cast<const float2*>(&s.row[token][space.at_pair(e)]);
+        second = fmaxf(fmaxf(second, w.y), fminf(first, w.x));
+        first = fmaxf(first, w.x);
+      }
+    } else {
+#pragma unroll 4
+      for (int e = g * a.per + part; e < g * a.per + a.per; e += parts) {
+        const float w = s.row[token][space.at(e)];
+        second = fmaxf(second, fminf(first, w));
+        first = fmaxf(first, w);
+      }
     }
     for (int p = 1; p < parts; p *= 2) {  // groups x parts lanes, all of them here
       const float w = __shfl_xor(first, p), u = __shfl_xor(second, p);
@@ -299,7 +326,7 @@ __device__ inline bool keep_groups(const SelectArgs& a, FewSpace<NE>& space, int
   }
   // past the last expert keys are closed already, whatever their group would be
   auto stays = [&](int i) { return kept >> (group_of(expert_at<16, V>(i, lane), a.magic) & 31) & 1; };
-  if (V > 1 && a.per % V == 0) {  // whole vectors
+  if (vectors) {
 #pragma unroll
     for (int i = 0; i < NE; i += V) {
       const bool out = !stays(i);
@@ -376,9 +403,14 @@ __global__ __launch_bounds__(kThreads) void select_kernel(SelectArgs a) {
         sum += v[i];
       }
     }
+    float lowest = lower[0];
 #pragma unroll
-    for (int i = 0; i < NE; ++i)
-      if (lower[i] == kClosed) key[i] = v[i] = kClosed;
+    for (int i = 1; i < NE; ++i) lowest = fminf(lowest, lower[i]);
+    if (__ballot(lowest == kClosed)) {
+#pragma unroll
+      for (int i = 0; i < NE; ++i)
+        if (lower[i] == kClosed) key[i] = v[i] = kClosed;
+    }
     doubt = !(sum == sum);  // a NaN somewhere
     if constexpr (Grouped) doubt = keep_groups<Scored, V>(a, space, token, lane, v, key) || doubt;
   } else {

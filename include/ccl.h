@@ -762,7 +762,10 @@ typedef struct {
  * picked may be NULL. A row whose target is negative is left out: its loss is 0 and it has no
  * part in a gradient; of a whole vocabulary, so is a target past its end. With a shard, picked
  * is 0 for a target that is no row of it, and loss has to be NULL: ccl_cross_entropy_join gives
- * it from all shards' lse and picked.
+ * it from all shards' lse and picked. A logit of -inf is no part of lse; one that is NaN or +inf
+ * makes its row's lse NaN. The workspace holds 8 bytes for 32 or 64 logits; of a small product
+ * (16 rows at most, or one whose sums are split) its fp32 sums, below 256 MiB.
+ * Errors: INVALID_ARGUMENT, UNSUPPORTED (dtype), HIP; the gradient's and the join's too.
  */
 int64_t ccl_linear_cross_entropy_workspace(const ccl_cross_entropy_desc* desc, int backward);
 int ccl_linear_cross_entropy(const ccl_cross_entropy_desc* desc, const void* x, const void* w, const int32_t* targets,
@@ -779,7 +782,9 @@ int ccl_cross_entropy_join(int shards, int64_t rows, const float* lse_parts, con
  * the whole vocabulary's (a shard's call gets the joined one; its dx is the shard's summand,
  * its dw its own). z is computed again, a piece of the vocabulary at a time: the workspace holds
  * dz of a piece, 512 MiB or 8192 columns of it. dz is rounded to the dtype for the two products,
- * as a stored gradient is; sums over pieces are fp32. dx or dw may be NULL.
+ * as a stored gradient is; sums over pieces are fp32. dz of a row left out is 0 whatever its x,
+ * dloss and lse hold, but x itself is a factor of dw's products: it has to be finite there too.
+ * dx or dw may be NULL.
  */
 int ccl_linear_cross_entropy_backward(const ccl_cross_entropy_desc* desc, const float* dloss, const void* x,
                                       const void* w, const int32_t* targets, const float* lse, void* dx, void* dw,
