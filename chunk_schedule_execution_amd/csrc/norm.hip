@@ -39,9 +39,11 @@ struct Pack {
       for (int q = 0; q < kValues; ++q) v[q] = q < left ? p[q] : T(0.0f);
     }
   }
+  template <bool Once = true>
   __device__ inline void store(T* p, int left) const {
     if (left >= kValues) {
-      __builtin_nontemporal_store(v, reinterpret_cast<vec*>(p));
+      if constexpr (Once) __builtin_nontemporal_store(v, reinterpret_cast<vec*>(p));
+      else *reinterpret_cast<vec*>(p) = v;
     } else {
 #pragma unroll
       for (int q = 0; q < kValues; ++q)
@@ -393,8 +395,8 @@ __global__ __launch_bounds__(Sharing<R>::kThreads) void norm_backward_kernel(Nor
         w.v[j] = dw[i][q + j];
         b.v[j] = db[i][q + j];
       }
-      w.store(to + c, width - c);
-      b.store(to + width + c, width - c);
+      w.template store<false>(to + c, width - c);  // read again at once
+      b.template store<false>(to + width + c, width - c);
     }
 }
 
