@@ -200,6 +200,43 @@ def test_cross_entropy_in_pieces(dtype, rows, k, vocabulary):
     within(dw, ww, bw, "dw")
 
 
+def test_cross_entropy_in_pieces_and_splits():
+    """Two pieces of the vocabulary whose dx is a few tiles of a long sum, so that each piece's
+    is split and the splits are added up over the pieces."""
+    rows, k, vocabulary = 2048, 64, 140000
+    x, w, targets = inputs(21, rows, k, vocabulary, "bf16")
+    _, lse = ops.linear_cross_entropy(x, w, targets)
+    targets[100:-100] = -1
+    dloss = normal(50, rows)
+    dx, dw = ops.linear_cross_entropy_backward(dloss, x, w, targets, lse)
+    assert not bool(dx[100:-100].any())
+    pick = torch.cat([torch.arange(100), torch.arange(rows - 100, rows)]).to("cuda:0")
+    xs, ts, ls, ds = x[pick], targets[pick], lse[pick], dloss[pick]
+    (wx, ww), (bx, bw) = loss_backward_bounds(*L.logits_gradient(ds, xs, w, ts, ls), xs, w, ls, k, x.dtype)
+    within(dx[pick], wx, bx + 64 * U32 * wx.abs(), "dx")
+    within(dw, ww, bw, "dw")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,k,vocabulary", [(3, 33, 50), (200, 128, 700)])
+def test_cross_entropy_of_rows_that_are_all_left_out(rows, k, vocabulary, dtype):
+    x, w, targets = inputs(23, rows, k, vocabulary, dtype)
+    targets.fill_(-1)
+    loss, lse = forward(x, w, targets)
+    assert not bool(loss.any())
+    for shard in (None, 0, 7):
+        dx, dw = ops.linear_cross_entropy_backward(normal(50, rows), x, w, targets, lse, shard=shard)
+        assert not bool(dx.any()) and not bool(dw.any())
+
+
+def test_cross_entropy_of_one_target_for_all_rows():
+    """Every row's gradient meets in one row of dw."""
+    x, w, targets = inputs(24, 300, 72, 500, "bf16")
+    targets.fill_(411)
+    _, lse = forward(x, w, targets)
+    backward(x, w, targets, lse)
+
+
 def test_cross_entropy_of_weights_past_31_bits():
     """A vocabulary whose matrix has more than 2^31 elements: its last rows count."""
     rows, k, vocabulary = 3, 4096, 530000

@@ -116,6 +116,19 @@ def test_norm_of_rows_far_from_zero(width):
     assert not bool(out[3].any()) and mean[3] == 5.0 and abs(float(rstd[3]) - 100.0) < 1e-3
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_norm_of_rows_of_zeros(dtype):
+    """Padding: such rows give the bias and, with no gradient of their own, add nothing."""
+    x = rows_of(1, 1100, 200, dtype)
+    w, b = parameters(200, dtype)
+    dout = normal(2, 1100, 200, dtype=TYPES[dtype])
+    x[600:], dout[600:] = 0.0, 0.0
+    out, mean, rstd = forward(x, w, b, None)
+    assert torch.equal(out[600:], b.expand(500, 200))
+    dx, _, _ = backward(x, w, None, dout, mean, rstd)
+    assert not bool(dx[600:].any())
+
+
 def test_norm_special_values():
     """Infinities and NaN stay in their row; gradients of columns take them up."""
     for rows, width in ((6, 300), (1030, 4096), (4, 20000)):
