@@ -196,7 +196,8 @@ __global__ __launch_bounds__(Sharing<R>::kThreads) void norm_kernel(NormArgs a) 
 }
 
 // Rows that registers do not hold: read three times, the second and third time from the
-// caches as far as they go. 1024 threads a row, 8 columns each at a time.
+// caches as far as they go, and nothing is written before the third, so that total and out may
+// take the inputs' places. 1024 threads a row, 8 columns each at a time.
 template <typename T>
 __device__ inline float block_sum(float v, float* parts) {
   v = over_sum<64>(v);
@@ -233,7 +234,6 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(NormArgs a) {
   for (int64_t c = threadIdx.x * 8; c < a.width; c += step) {
     const int n = int(min(int64_t(8), a.width - c));
     read(c, n, h);
-    if (total) store8(total + c, vec_t, n, h);
 #pragma unroll
     for (int q = 0; q < 8; ++q) sum += h[q];
   }
@@ -253,6 +253,7 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(NormArgs a) {
     const int n = int(min(int64_t(8), a.width - c));
     float v[8];
     read(c, n, h);
+    if (total) store8(total + c, vec_t, n, h);
 #pragma unroll
     for (int q = 0; q < 8; ++q) h[q] = (h[q] - mean) * rstd;
     if (a.weight) {

@@ -727,7 +727,8 @@ typedef struct {
  * out = (h - mean) rstd weight + bias with h = x + residual, mean and rstd = (variance +
  * eps)^-1/2 over a row's `width` values, in fp32 (the variance from differences to the mean).
  * residual, weight and bias may be NULL. total (NULL, or with a residual): receives h, rounded
- * to the dtype; the norm sees it unrounded. mean, rstd (both or neither): fp32 by row.
+ * to the dtype; the norm sees it unrounded. mean, rstd (both or neither): fp32 by row. out and
+ * total may each be x or residual, with the same row distance.
  * Errors: INVALID_ARGUMENT, UNSUPPORTED, HIP.
  */
 int ccl_layer_norm(const ccl_norm_desc* desc, const void* x, const void* residual, const void* weight,

@@ -221,3 +221,24 @@ def test_norm_graph_replays_and_streams():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(held, want)), i
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,width,pad", [(3, 72, 0), (1030, 1000, 3), (3, 20001, 1), (1100, 17000, 0)])
+def test_norm_in_place(rows, width, pad, dtype):
+    """total onto the residual (or x) and out onto the other: the same bits as apart."""
+    w, b = parameters(width, dtype)
+
+    def inputs():
+        return rows_of(1, rows, width, dtype, pad), rows_of(3, rows, width, dtype, pad)
+
+    x, r = inputs()
+    want = ops.layer_norm(x, weight=w, bias=b, residual=r, save_stats=True)
+    alone = ops.layer_norm(x, weight=w, bias=b)
+    for total_onto_x in (False, True):
+        x, r = inputs()
+        out, total = (r, x) if total_onto_x else (x, r)
+        got = ops.layer_norm(x, weight=w, bias=b, residual=r, save_stats=True, out=out, total=total)
+        assert got[0] is out and got[1] is total and all(torch.equal(p, q) for p, q in zip(got, want))
+    x, _ = inputs()
+    assert torch.equal(ops.layer_norm(x, weight=w, bias=b, out=x), alone)
