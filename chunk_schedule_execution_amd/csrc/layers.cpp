@@ -184,7 +184,9 @@ LossPlan loss_plan(const ccl_cross_entropy_desc& d, bool backward) {
       return p;
     }
   }
-  p.copy_x = off || d.ld_x % v || d.in_features % v;
+  // The gradients' x is always a copy, with zeros in the rows that are left out: their dz is 0,
+  // but 0 times what a row of padding may hold, NaN or infinite, would reach dw.
+  p.copy_x = backward || off || d.ld_x % v || d.in_features % v;
   p.copy_w = off || d.ld_w % v || d.in_features % v;
   p.ld_x = p.copy_x ? up(d.in_features) : d.ld_x;
   p.ld_w = p.copy_w ? up(d.in_features) : d.ld_w;
@@ -215,13 +217,13 @@ LossPlan loss_plan(const ccl_cross_entropy_desc& d, bool backward) {
   return p;
 }
 
-// x and w, or their copies on the 16-byte grid.
-void operands(const ccl_cross_entropy_desc& d, const LossPlan& p, unsigned char* space, void* stream, const void** x,
-              const void** w) {
+// x and w, or their copies on the 16-byte grid, x's without the rows that l (or NULL) leaves out.
+void operands(const ccl_cross_entropy_desc& d, const LossPlan& p, const LossArgs* l, unsigned char* space, void* stream,
+              const void** x, const void** w) {
   Regrid copy[2];
   int copies = 0;
   if (p.copy_x) {
-    copy[copies++] = {*x, space, d.ld_x, d.rows, d.in_features, p.ld_x};
+    copy[copies++] = {*x, space, d.ld_x, d.rows, d.in_features, p.ld_x, l ? l->targets : nullptr, l ? l->end : 0};
     *x = space;
   }
   if (p.copy_w) {
@@ -274,7 +276,7 @@ int loss_forward(const ccl_cross_entropy_desc* desc, const void* x, const void* 
     launched(launch_loss_rows(r, l, stream, &err), err);
     return CCL_OK;
   }
-  operands(d, p, space, stream, &x, &w);
+  operands(d, p, nullptr, space, stream, &x, &w);
   const ProductKind kind = unsplit_tile(d.dtype, g);
   g.a = x;
   g.b = w;
@@ -315,9 +317,9 @@ int loss_backward(const ccl_cross_entropy_desc* desc, const float* dloss, const 
   check_workspace(ws, ws_bytes, p.total);
   unsigned char* const space = static_cast<unsigned char*>(ws);
   std::string err;
-  if (d.rows > 0) operands(d, p, space, stream, &x, &w);
-  const int64_t size = elem_size(d.dtype), v = 16 / size;
   LossArgs l = loss_args(d, targets);
+  if (d.rows > 0) operands(d, p, &l, space, stream, &x, &w);
+  const int64_t size = elem_size(d.dtype), v = 16 / size;
   l.lse = lse;
   l.dloss = dloss;
   const int first = l.first;

@@ -70,6 +70,8 @@ struct Regrid {
   const void* src = nullptr;
   void* dst = nullptr;
   int64_t ld = 0, rows = 0, len = 0, ld_dst = 0;
+  const int32_t* targets = nullptr;  // or NULL: a row whose target is none below end becomes zeros
+  unsigned end = 0;
 };
 int launch_regrid(int dtype, const Regrid& first, const Regrid& second, void* stream, std::string* err);
 // The results of a product from its splits' sums in args.partial.

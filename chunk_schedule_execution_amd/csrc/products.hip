@@ -32,8 +32,9 @@ __global__ __launch_bounds__(256) void regrid_kernel(Regrid first, Regrid second
   const int n = int(max(int64_t(0), min(int64_t(V), g.len - at)));
   for (int64_t r = int64_t(blockIdx.x) * blockDim.y + threadIdx.y; r < g.rows; r += int64_t(gridDim.x) * blockDim.y) {
     const T* src = static_cast<const T*>(g.src) + r * g.ld + at;
-    wide v;
-    if (n == V) {
+    wide v = {};
+    if (g.targets && unsigned(g.targets[r]) >= g.end) {
+    } else if (n == V) {
       v = *reinterpret_cast<const wide_anywhere*>(src);
     } else {
 #pragma unroll

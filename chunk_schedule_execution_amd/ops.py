@@ -575,7 +575,7 @@ def linear_cross_entropy_backward(dloss, x, w, targets, lse, shard=None, need_dx
     float32; lse is the whole vocabulary's. The logits are computed again, in pieces of the
     vocabulary. With ``shard`` dx is this shard's summand (an AllReduce adds them up), dw its
     own. dz is rounded to the tensors' type for the two products, as ``linear_backward``'s is.
-    Rows left out have no part, whatever their dloss and lse hold; their x has to be finite."""
+    Rows left out have no part, whatever their x, dloss and lse hold."""
     device = _first(x, "x")
     d, pt = _loss_desc(x, w, targets, shard, device)
     rows = x.shape[0]

@@ -783,9 +783,8 @@ int ccl_cross_entropy_join(int shards, int64_t rows, const float* lse_parts, con
  * the whole vocabulary's (a shard's call gets the joined one; its dx is the shard's summand,
  * its dw its own). z is computed again, a piece of the vocabulary at a time: the workspace holds
  * dz of a piece, 512 MiB or 8192 columns of it. dz is rounded to the dtype for the two products,
- * as a stored gradient is; sums over pieces are fp32. dz of a row left out is 0 whatever its x,
- * dloss and lse hold, but x itself is a factor of dw's products: it has to be finite there too.
- * dx or dw may be NULL.
+ * as a stored gradient is; sums over pieces are fp32. A row left out has no part whatever its x,
+ * dloss and lse hold, NaN included. dx or dw may be NULL.
  */
 int ccl_linear_cross_entropy_backward(const ccl_cross_entropy_desc* desc, const float* dloss, const void* x,
                                       const void* w, const int32_t* targets, const float* lse, void* dx, void* dw,

@@ -319,3 +319,31 @@ def test_cross_entropy_graph_replays_and_streams():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(held, want)), i
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,k,vocabulary,pad", [(3, 64, 50, 0), (9, 33, 700, 1), (200, 128, 700, 0), (300, 65, 1000, 1),
+                                                   (1100, 264, 2500, 8)])
+def test_cross_entropy_of_left_out_rows_of_nan(rows, k, vocabulary, pad, dtype):
+    """What padding holds reaches neither another row's loss nor a gradient, to the bit."""
+    x, w, targets = inputs(31, rows, k, vocabulary, dtype, pad=pad)
+    targets[1] = -1
+    out = targets < 0
+    dloss = normal(50, rows)
+    for shard in (None, 7):
+        clean = ops.linear_cross_entropy(x, w, targets, shard=shard)
+        lse = clean[1] if shard is None else clean[0]
+        want = ops.linear_cross_entropy_backward(dloss, x, w, targets, lse, shard=shard)
+        for value in (float("nan"), float("inf"), -3e38):
+            y = x.clone()
+            y[out] = value
+            got = ops.linear_cross_entropy(y, w, targets, shard=shard)
+            assert all(torch.equal(a[~out], b[~out]) for a, b in zip(got, clean))
+            if shard is None:
+                assert not bool(got[0][out].any())
+            got = ops.linear_cross_entropy_backward(dloss, y, w, targets, got[1] if shard is None else got[0], shard=shard)
+            assert all(torch.equal(a, b) for a, b in zip(got, want)) and not bool(got[0][out].any())
+            # one gradient alone as well
+            for only in (dict(need_dx=False), dict(need_dw=False)):
+                alone = ops.linear_cross_entropy_backward(dloss, y, w, targets, lse, shard=shard, **only)
+                assert torch.equal(alone[0], want[1 if "need_dx" in only else 0])
