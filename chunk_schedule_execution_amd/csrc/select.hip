@@ -116,7 +116,7 @@ __device__ inline void choose_whole(const SelectArgs& a, int64_t t, WholeSpace<N
   float x[NE];
   load_row<64, 1>(static_cast<const T*>(a.logits) + t * a.ld, lane, a.experts, kClosed, x);
   const bool soft = a.score == CCL_SCORE_SOFTMAX, grouped = a.kept < a.groups;
-  const bool scored = a.bias || (grouped && a.best == 2);
+  const bool scored = a.bias || grouped;
   const float top = row_top<64>(x);
   double total = 0.0;
   if (scored && soft) {
@@ -259,11 +259,23 @@ struct FewSpace {
 // argument, and 2^-24 p for each of the sum's at most 35 additions and for the functions.
 __device__ inline float value_off(bool soft) { return soft ? 0x1p-18f : 0x1p-22f; }
 
+// Whether scores differ in 64 bits where the logits do, high > low: they come in the logits'
+// order, but sigmoids near 1, terms of a softmax near 0 and any two of nearly the same logit
+// round to the same value. In a softmax the scores' quotient is above 1 + high - low, and each
+// is off by 2^-53 of low - top and a few steps of 2^-53. Sigmoids differ by a sixteenth of the
+// logits' difference (1 at most) of p (1 - p) at least, each off by a few steps.
+__device__ inline bool scores_differ(float high, float low, float top, bool soft) {
+  const float gap = high - low;
+  if (soft) return low - top > -600.0f && gap > 0x1p-48f * (2.0f + (top - low));
+  return low > -600.0f && fminf(gap, 1.0f) * exp_exact(-fmaxf(low, 0.0f)) > 0x1p-45f;
+}
+
 // Takes the keys of experts outside the kept groups away; true where fp32 cannot tell which
-// those are. v: the experts' values, exact where they are the logits.
+// those are. v: the experts' values, or (not Scored) their logits, whose order groups of one
+// best score have too, but for equal scores. top: the row's highest logit.
 template <bool Scored, int V, int NE>
 __device__ inline bool keep_groups(const SelectArgs& a, FewSpace<NE>& space, int token, int lane, const float (&v)[NE],
-                                   float (&key)[NE]) {
+                                   float (&key)[NE], float top) {
   auto& s = space.few;
   const int groups = a.groups, parts = 1 << a.parts_log2;
   const bool vectors = V > 1 && a.per % V == 0;  // no vector lies in two groups
@@ -338,16 +350,34 @@ __device__ inline bool keep_groups(const SelectArgs& a, FewSpace<NE>& space, int
     for (int i = 0; i < NE; ++i)
       if (!stays(i)) key[i] = kClosed;
   }
-  if (!Scored) return false;
   lowest = -over_max<16>(-lowest);
   highest = over_max<16>(highest);
+  if constexpr (!Scored) {
+    // No group that goes may have the score of one that stays by a higher logit. The nearest
+    // such pairs: the lowest that stays above the highest that goes, and the reverse; one pair,
+    // but where the two are the same. 16384 x 256 fp32 softmax, 4 of 8 groups: 14.7 -> 15.7 us.
+    const bool soft = a.score == CCL_SCORE_SOFTMAX;
+    float above = INFINITY, below = kClosed, best = kClosed;
+    for (int g = lane; g < groups; g += 16) {
+      const float w = s.best[token][g];
+      best = fmaxf(best, w);
+      if (w > highest) above = fminf(above, w);
+      if (w < lowest) below = fmaxf(below, w);
+    }
+    above = -over_max<16>(-above);
+    below = over_max<16>(below);
+    best = over_max<16>(best);
+    // infinite: or NaN, which ranks as that
+    return best == INFINITY || (highest > kClosed && above < INFINITY && !scores_differ(above, highest, top, soft)) ||
+           (below > kClosed && !scores_differ(lowest, below, top, soft));
+  }
   size = over_max<16>(size);
   // on either side two values and their sum: 2 offs, and 2^-24 of the size for each addition
   return highest > kClosed && !(lowest - highest > 4 * value_off(a.score == CCL_SCORE_SOFTMAX) + 0x1p-22f * size);
 }
 
-// Scored: experts are ranked by p + bias, or groups by sums of p. Otherwise by their logits,
-// which fp32 holds as they are.
+// Scored: experts are ranked by p + bias, or groups by sums of p. Otherwise both by their
+// logits, which fp32 holds as they are.
 template <typename T, bool Scored, bool Grouped, int NE, int V>
 __global__ __launch_bounds__(kThreads) void select_kernel(SelectArgs a) {
   __shared__ FewSpace<NE> spaces[kThreads / 64];
@@ -412,7 +442,7 @@ __global__ __launch_bounds__(kThreads) void select_kernel(SelectArgs a) {
         if (lower[i] == kClosed) key[i] = v[i] = kClosed;
     }
     doubt = !(sum == sum);  // a NaN somewhere
-    if constexpr (Grouped) doubt = keep_groups<Scored, V>(a, space, token, lane, v, key) || doubt;
+    if constexpr (Grouped) doubt = keep_groups<Scored, V>(a, space, token, lane, v, key, top) || doubt;
   } else {
 #pragma unroll
     for (int i = 0; i < NE; ++i) key[i] = nan_first(x[i]);
@@ -420,7 +450,7 @@ __global__ __launch_bounds__(kThreads) void select_kernel(SelectArgs a) {
       float v[NE];
 #pragma unroll
       for (int i = 0; i < NE; ++i) v[i] = key[i];
-      keep_groups<Scored, V>(a, space, token, lane, v, key);
+      doubt = keep_groups<Scored, V>(a, space, token, lane, v, key, top);
     }
   }
 

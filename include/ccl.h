@@ -694,11 +694,13 @@ typedef struct {
 /*
  * The choice of experts. p = softmax of a token's logits over all experts, or their sigmoids.
  * Experts are ranked by p + bias (bias: fp32 by expert, or NULL), compared in 64 bits; without
- * a bias by their logits, which is the same order. With kept_groups < groups, only the experts
- * of the kept_groups groups of highest value stay, a group's value being the sum of the
- * group_best highest values p + bias of its experts. The `choices` highest of what stays are
- * chosen, in descending order; ties go to the lower index. gates = scale p of the chosen ones,
- * divided by the sum of their p with renormalise; the bias is no part of a gate.
+ * a bias by their logits, whose order is that of p but for p that round to the same value. With
+ * kept_groups < groups, only the experts of the kept_groups groups of highest value stay, a
+ * group's value being the sum of the group_best highest values p + bias of its experts, in 64
+ * bits with a bias or without: groups of sigmoids that round to 1 tie, whatever the logits. The
+ * `choices` highest of what stays are chosen, in descending order; ties go to the lower index.
+ * gates = scale p of the chosen ones, divided by the sum of their p with renormalise; the bias
+ * is no part of a gate.
  * An expert whose logit or bias is -inf is closed: it is never chosen and adds nothing to a
  * group. Where fewer than `choices` are open, the rest of the token's ids are -1 (which
  * ccl_expert_route reads as no row) and their gates 0. A NaN ranks as +inf; the gates that
