@@ -14,11 +14,15 @@ namespace {
 
 constexpr float kLog2e = 1.44269504088896341f;
 
-// exp(z - base), base2 = base log2(e), by the hardware's power of 2: one rounding of the
-// argument, so off by 2^-24 of |z - base| and of |base| and a step.
-__device__ inline float exp_from(float z, float base2) {
-  return __builtin_amdgcn_exp2f(fmaf(z, kLog2e, -base2));
-}
+// exp(z - base) by the hardware's power of 2: one rounding of the argument, so off by 2^-24 of
+// |z - base| and of |base| and a step. Where base log2(e) may be past fp32's range, values are
+// 2^102 apart and more: z is base or so far off that any power is 1 or 0.
+struct ExpFrom {
+  float scale, base2;
+  __device__ inline explicit ExpFrom(float base)
+      : scale(fabsf(base) < 0x1p126f ? kLog2e : 1.0f), base2(base * scale) {}
+  __device__ inline float operator()(float z) const { return __builtin_amdgcn_exp2f(fmaf(z, scale, -base2)); }
+};
 
 // Column of a target, negative where there is none.
 __device__ inline int target_column(int target, int first) { return target < 0 ? -1 : max(-1, target - first); }
@@ -71,12 +75,12 @@ struct RowSums {
         for (int q = 0; q < 4; ++q) m = fmaxf(m, acc[i][j][q]);
       m = fmaxf(m, __shfl_xor(m, 16));
       m = fmaxf(m, __shfl_xor(m, 32));
-      const float base2 = m == -INFINITY ? 0.0f : m * kLog2e;
+      const ExpFrom exp_from(m == -INFINITY ? 0.0f : m);
       float sum = 0.0f;
 #pragma unroll
       for (int j = 0; j < FN; ++j)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) sum += exp_from(acc[i][j][q], base2);
+        for (int q = 0; q < 4; ++q) sum += exp_from(acc[i][j][q]);
       sum += __shfl_xor(sum, 16);
       sum += __shfl_xor(sum, 32);
       if (in >= job.m_end - job.row) continue;
@@ -129,11 +133,11 @@ struct LossSlope {
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
       const bool out = rows.at[i] == INT_MIN;
-      const float lse2 = rows.lse[i] * kLog2e;
+      const ExpFrom exp_from(rows.lse[i]);
 #pragma unroll
       for (int j = 0; j < FN; ++j)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) acc[i][j][q] = out ? 0.0f : rows.d[i] * exp_from(acc[i][j][q], lse2);
+        for (int q = 0; q < 4; ++q) acc[i][j][q] = out ? 0.0f : rows.d[i] * exp_from(acc[i][j][q]);
       const int at = out ? -1 : rows.at[i] - first;
       if (__ballot(at >= 0 && at < FN * 16)) {  // of a row's columns few waves hold the target
 #pragma unroll
