@@ -5,6 +5,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <cstdlib>
 
 #include "args.h"
 
@@ -67,6 +68,39 @@ NormArgs norm_args(const ccl_norm_desc* d) {
   a.ld_dtotal = stride_of(d->ld_dtotal, d->width, "ld_dtotal");
   a.ld_dx = stride_of(d->ld_dx, d->width, "ld_dx");
   return a;
+}
+
+// Whether two matrices of `rows` rows of `width` bytes, their rows ld_p and ld_q bytes apart,
+// have a byte in common. Rows side by side in one buffer do not.
+bool share_memory(const void* p, int64_t ld_p, const void* q, int64_t ld_q, int64_t rows, int64_t width) {
+  const int64_t from = int64_t(reinterpret_cast<uintptr_t>(q) - reinterpret_cast<uintptr_t>(p));
+  if (from >= (rows - 1) * ld_p + width || -from >= (rows - 1) * ld_q + width) return false;
+  auto floor_div = [](int64_t a, int64_t b) { return a / b - (a % b < 0); };
+  if (ld_p == ld_q) {  // rows of p this many behind q's, or one more
+    const int64_t behind = floor_div(from, ld_p), off = from - behind * ld_p;
+    return (std::abs(behind) < rows && off < width) || (std::abs(behind + 1) < rows && ld_p - off < width);
+  }
+  for (int64_t row = 0; row < rows; ++row) {
+    // the first of p's rows that ends behind this one of q's begins
+    const int64_t at = from + row * ld_q, first = std::max<int64_t>(0, floor_div(at - width, ld_p) + 1);
+    if (first < rows && first * ld_p < at + width) return true;
+  }
+  return false;
+}
+// The norm's outputs may take its inputs' places whole, and otherwise no memory of theirs or of
+// each other: rows are read by one workgroup while others write.
+void in_place_or_apart(const NormArgs& a, int size) {
+  auto share = [&](const void* p, int64_t ld_p, const void* q, int64_t ld_q) {
+    return p && q && share_memory(p, ld_p * size, q, ld_q * size, a.rows, a.width * size);
+  };
+  auto taken = [&](const void* p, int64_t ld_p, const void* q, int64_t ld_q) {
+    return !(p == q && (ld_p == ld_q || a.rows == 1)) && share(p, ld_p, q, ld_q);
+  };
+  require(!share(a.out, a.ld_out, a.total, a.ld_total), "out and total: the same memory");
+  require(!taken(a.out, a.ld_out, a.x, a.ld_x), "out: memory of x, but not x itself");
+  require(!taken(a.out, a.ld_out, a.residual, a.ld_residual), "out: memory of residual, but not residual itself");
+  require(!taken(a.total, a.ld_total, a.x, a.ld_x), "total: memory of x, but not x itself");
+  require(!taken(a.total, a.ld_total, a.residual, a.ld_residual), "total: memory of residual, but not residual itself");
 }
 int64_t norm_workspace(const NormArgs& a) { return align16(norm_partials(a.rows) * 2 * a.width * 4); }
 
@@ -439,6 +473,7 @@ int ccl_layer_norm(const ccl_norm_desc* desc, const void* x, const void* residua
     a.total = total;
     a.mean = mean;
     a.rstd = rstd;
+    in_place_or_apart(a, size);
     std::string err;
     launched(launch_norm(desc->dtype, a, stream, &err), err);
     return CCL_OK;

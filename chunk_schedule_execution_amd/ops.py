@@ -437,8 +437,8 @@ def layer_norm(x, weight=None, bias=None, residual=None, eps=1e-5, save_stats=Fa
     weight and bias (width,). Returns out; with a residual also total, h rounded to the type
     (the norm sees it unrounded); with ``save_stats`` also mean and rstd, (rows,) float32:
     (out[, total][, mean, rstd]). ``layer_norm_backward`` takes total (x without a residual)
-    and the statistics. ``out`` and ``total`` may be given, also as x or residual themselves.
-    Autograd does not see the call."""
+    and the statistics. ``out`` and ``total`` may be given, also as x or residual themselves (not
+    both as the same one, nor as other rows of their memory). Autograd does not see the call."""
     device = _first(x, "x")
     rows, width = x.shape
     dtype = x.dtype

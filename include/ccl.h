@@ -730,7 +730,8 @@ typedef struct {
  * eps)^-1/2 over a row's `width` values, in fp32 (the variance from differences to the mean).
  * residual, weight and bias may be NULL. total (NULL, or with a residual): receives h, rounded
  * to the dtype; the norm sees it unrounded. mean, rstd (both or neither): fp32 by row. out and
- * total may each be x or residual, with the same row distance.
+ * total may each be x or residual, with the same row distance; otherwise they share no memory
+ * with those or with each other (rows side by side in one buffer do not), or the call is refused.
  * Errors: INVALID_ARGUMENT, UNSUPPORTED, HIP.
  */
 int ccl_layer_norm(const ccl_norm_desc* desc, const void* x, const void* residual, const void* weight,
