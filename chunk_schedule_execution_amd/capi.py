@@ -47,6 +47,7 @@ CCL_I_SKIP, CCL_I_NOFLAG = 0x20, 0x40
 CCL_ACT_NONE, CCL_ACT_RELU, CCL_ACT_GELU, CCL_ACT_GELU_TANH, CCL_ACT_SILU = range(5)
 CCL_LINEAR_UNALIGNED = 0x1
 CCL_SCORE_SOFTMAX, CCL_SCORE_SIGMOID = range(2)
+CCL_GRADIENTS, CCL_GRADIENT_DX, CCL_GRADIENT_DW = 1, 2, 3
 
 
 class ccl_chunk_op(C.Structure):
@@ -521,8 +522,8 @@ def ccl_layer_norm_backward(desc: ccl_norm_desc, dout: int, x: int, mean: int, r
                                         workspace, workspace_bytes, stream), "ccl_layer_norm_backward")
 
 
-def ccl_linear_cross_entropy_workspace(desc: ccl_cross_entropy_desc, backward: bool) -> int:
-    v = _lib.ccl_linear_cross_entropy_workspace(C.byref(desc), int(bool(backward)))
+def ccl_linear_cross_entropy_workspace(desc: ccl_cross_entropy_desc, backward: int) -> int:
+    v = _lib.ccl_linear_cross_entropy_workspace(C.byref(desc), int(backward))
     if v < 0:
         _check(int(v), "ccl_linear_cross_entropy_workspace")
     return int(v)

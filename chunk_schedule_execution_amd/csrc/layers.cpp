@@ -139,7 +139,7 @@ int64_t piece_columns(const ccl_cross_entropy_desc& d) {
 
 // Where the parts of a call's workspace lie and how its products are run.
 struct LossPlan {
-  bool copy_x = false, copy_w = false;  // onto the 16-byte grid
+  bool copy_x = false, copy_w = false;  // onto the 16-byte grid, or x for its zeroed rows
   int64_t ld_x = 0, ld_w = 0;
   int64_t at_w = 0, at_sums = 0, at_picked = 0;              // forward
   int64_t at_dz = 0, at_dx = 0, at_product = 0, ld_dz = 0;   // backward
@@ -202,8 +202,14 @@ int64_t logits_bytes(const ProductPlan& p, const ProductArgs& g) {
   return p.at_partial + p.splits * g.m * partial_ld(g.n) * 4;
 }
 
-LossPlan loss_plan(const ccl_cross_entropy_desc& d, bool backward) {
+// What a call gives: the loss, or gradients.
+struct LossGives {
+  bool backward = false, dx = false, dw = false;
+};
+
+LossPlan loss_plan(const ccl_cross_entropy_desc& d, const LossGives& gives) {
   LossPlan p;
+  const bool backward = gives.backward;
   const int64_t size = elem_size(d.dtype), v = 16 / size;
   auto up = [&](int64_t n) { return (n + v - 1) / v * v; };
   const bool off = d.flags & CCL_LINEAR_UNALIGNED;
@@ -218,9 +224,10 @@ LossPlan loss_plan(const ccl_cross_entropy_desc& d, bool backward) {
       return p;
     }
   }
-  // The gradients' x is always a copy, with zeros in the rows that are left out: their dz is 0,
-  // but 0 times what a row of padding may hold, NaN or infinite, would reach dw.
-  p.copy_x = backward || off || d.ld_x % v || d.in_features % v;
+  // dw's x is always a copy, with zeros in the rows that are left out: their dz is 0, but 0 times
+  // what a row of padding may hold, NaN or infinite, would reach dw. (dz itself is set to 0 in
+  // such rows, whatever their logits.)
+  p.copy_x = gives.dw || off || d.ld_x % v || d.in_features % v;
   p.copy_w = off || d.ld_w % v || d.in_features % v;
   p.ld_x = p.copy_x ? up(d.in_features) : d.ld_x;
   p.ld_w = p.copy_w ? up(d.in_features) : d.ld_w;
@@ -235,15 +242,15 @@ LossPlan loss_plan(const ccl_cross_entropy_desc& d, bool backward) {
   }
   p.piece = piece_columns(d);
   p.ld_dz = up(std::min(p.piece, d.vocabulary));
-  p.onto = p.piece < d.vocabulary;
+  p.onto = gives.dx && p.piece < d.vocabulary;
   p.at_dz = copied;
   p.dx = plan_product(d.dtype, false, true, kPlain, dx_args(d, p, std::min(p.piece, d.vocabulary)), kPadded, kPadded);
   p.at_dx = p.at_dz + align16(d.rows * p.ld_dz * size);
   p.at_product = p.at_dx + (p.onto ? p.dx.splits * d.rows * partial_ld(d.in_features) * 4 : 0);
-  int64_t most = p.onto ? 0 : p.dx.bytes;
+  int64_t most = p.onto || !gives.dx ? 0 : p.dx.bytes;
   for (int64_t lo = 0; lo < d.vocabulary; lo += p.piece) {
     const int64_t n = std::min(p.piece, d.vocabulary - lo);
-    most = std::max(most, dw_plan(d, p, n).bytes);
+    if (gives.dw) most = std::max(most, dw_plan(d, p, n).bytes);
     const ProductPlan logits = logits_plan(d, p, n);
     if (through_memory(logits, logits_args(d, p, n))) most = std::max(most, logits_bytes(logits, logits_args(d, p, n)));
   }
@@ -288,7 +295,7 @@ int loss_forward(const ccl_cross_entropy_desc* desc, const void* x, const void* 
   optional_elements(4, loss, "loss: misaligned");
   optional_elements(4, picked, "picked: misaligned");
   require(!loss || d.first < 0, "loss: of a whole vocabulary only; join the shards' sums first");
-  const LossPlan p = loss_plan(d, false);
+  const LossPlan p = loss_plan(d, {});
   check_workspace(ws, ws_bytes, p.total);
   unsigned char* const space = static_cast<unsigned char*>(ws);
   std::string err;
@@ -347,12 +354,12 @@ int loss_backward(const ccl_cross_entropy_desc* desc, const float* dloss, const 
   aligned(d, w, "w");
   aligned(d, dx, "dx");
   aligned(d, dw, "dw");
-  const LossPlan p = loss_plan(d, true);
+  const LossPlan p = loss_plan(d, {true, dx != nullptr, dw != nullptr});
   check_workspace(ws, ws_bytes, p.total);
   unsigned char* const space = static_cast<unsigned char*>(ws);
   std::string err;
   LossArgs l = loss_args(d, targets);
-  if (d.rows > 0) operands(d, p, &l, space, stream, &x, &w);
+  if (d.rows > 0) operands(d, p, dw ? &l : nullptr, space, stream, &x, &w);
   const int64_t size = elem_size(d.dtype), v = 16 / size;
   l.lse = lse;
   l.dloss = dloss;
@@ -527,7 +534,8 @@ int ccl_layer_norm_backward(const ccl_norm_desc* desc, const void* dout, const v
 int64_t ccl_linear_cross_entropy_workspace(const ccl_cross_entropy_desc* desc, int backward) {
   int64_t bytes = 0;
   const int rc = api_guarded([&] {
-    bytes = loss_plan(checked(desc), backward != 0).total;
+    const bool any = backward != 0;
+    bytes = loss_plan(checked(desc), {any, any && backward != CCL_GRADIENT_DW, any && backward != CCL_GRADIENT_DX}).total;
     return CCL_OK;
   });
   return rc ? rc : bytes;

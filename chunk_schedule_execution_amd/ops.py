@@ -584,7 +584,8 @@ def linear_cross_entropy_backward(dloss, x, w, targets, lse, shard=None, need_dx
     with on as handle:
         dx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if need_dx else None
         dw = torch.empty(w.shape, dtype=x.dtype, device=x.device) if need_dw else None
-        nbytes = capi.ccl_linear_cross_entropy_workspace(d, True)
+        nbytes = capi.ccl_linear_cross_entropy_workspace(
+            d, capi.CCL_GRADIENTS if need_dx and need_dw else capi.CCL_GRADIENT_DX if need_dx else capi.CCL_GRADIENT_DW)
         ws = _workspace(nbytes, x.device)
         capi.ccl_linear_cross_entropy_backward(d, pd, x.data_ptr(), w.data_ptr(), pt, pl, dx.data_ptr() if need_dx else 0,
                                                dw.data_ptr() if need_dw else 0, ws.data_ptr() if nbytes else 0, nbytes,

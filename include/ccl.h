@@ -760,6 +760,11 @@ typedef struct {
   int64_t ld_x, ld_w, ld_dx, ld_dw;
 } ccl_cross_entropy_desc;
 
+/* What ccl_linear_cross_entropy_workspace is asked for (0: the loss). */
+#define CCL_GRADIENTS 1   /* either gradient, or both */
+#define CCL_GRADIENT_DX 2 /* calls without dw */
+#define CCL_GRADIENT_DW 3 /* calls without dx */
+
 /*
  * Cross entropy of z = x w^T against targets (int32 by row) without keeping z: lse = log sum
  * exp z over w's rows, picked = z at the target, loss = lse - picked, all fp32 by row. loss and
