@@ -309,12 +309,6 @@ __global__ __launch_bounds__(256) void combine_backward_kernel(const T* dout, in
   }
 }
 
-// A grid of n workgroups: one dimension holds less than 2^32 threads.
-inline dim3 flat_grid(int64_t n) {
-  const int64_t x = std::min<int64_t>(n, 1 << 20);
-  return dim3(unsigned(x), unsigned((n + x - 1) / x));
-}
-
 // Whether rows of `width` elements at base p, ld apart, are whole 16-byte vectors.
 inline bool on_grid(const void* p, int64_t ld, int64_t width, int size) {
   return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * size % 16 == 0 && width * size % 16 == 0;

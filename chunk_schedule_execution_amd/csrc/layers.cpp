@@ -399,7 +399,8 @@ int loss_backward(const ccl_cross_entropy_desc* desc, const float* dloss, const 
         launched(launch_product(d.dtype, false, true, kPlain, g, p.dx, space + p.at_product, stream, &err), err);
       } else {
         g.partial = reinterpret_cast<float*>(space + p.at_dx);
-        launched(launch_product_onto(d.dtype, g, p.dx, lo == 0, stream, &err), err);
+        launched(lo == 0 ? launch_product_sums(d.dtype, false, true, kPlain, g, p.dx, nullptr, stream, &err)
+                         : launch_product_onto(d.dtype, g, p.dx, stream, &err), err);
         if (lo + n == d.vocabulary) launched(launch_join(d.dtype, g, p.dx.splits, stream, &err), err);
       }
     }

@@ -85,9 +85,8 @@ struct LossRowsArgs {
 };
 int launch_loss_rows(const LossRowsArgs& args, const LossArgs& loss, void* stream, std::string* err);
 int launch_loss_rows_slope(int dtype, const LossRowsArgs& args, const LossArgs& loss, void* stream, std::string* err);
-// A b_by_k product whose sums are written to g.partial (fresh) or added to what is there.
-int launch_product_onto(int dtype, const ProductArgs& g, const ProductPlan& plan, bool fresh, void* stream,
-                        std::string* err);
+// A b_by_k product whose sums are added to what is in g.partial.
+int launch_product_onto(int dtype, const ProductArgs& g, const ProductPlan& plan, void* stream, std::string* err);
 
 // Joins parts of the rows' sums: `blocks` rows of pairs in `pairs`, or (pairs NULL) `blocks`
 // rows of lse_parts and picked_parts, which are one shard's each. n: the columns that targets

@@ -15,8 +15,8 @@ int loss_slope_bf16(const ProductArgs& g, const LossArgs& loss, int64_t padded, 
                     std::string* err);
 int loss_slope_f32(const ProductArgs& g, const LossArgs& loss, int64_t padded, ProductKind kind, hipStream_t s,
                    std::string* err);
-int product_onto_bf16(const ProductArgs& g, const ProductPlan& plan, bool fresh, hipStream_t s, std::string* err);
-int product_onto_f32(const ProductArgs& g, const ProductPlan& plan, bool fresh, hipStream_t s, std::string* err);
+int product_onto_bf16(const ProductArgs& g, const ProductPlan& plan, hipStream_t s, std::string* err);
+int product_onto_f32(const ProductArgs& g, const ProductPlan& plan, hipStream_t s, std::string* err);
 
 namespace {
 
@@ -170,11 +170,6 @@ __global__ __launch_bounds__(256) void loss_rows_slope_kernel(LossRowsArgs a, Lo
   *reinterpret_cast<four*>(static_cast<T*>(a.dz) + row * a.ldz + c) = o;
 }
 
-inline dim3 flat_grid(int64_t n) {
-  const int64_t x = std::min<int64_t>(n, 1 << 20);
-  return dim3(unsigned(x), unsigned((n + x - 1) / x));
-}
-
 }  // namespace
 }  // namespace prod
 
@@ -193,9 +188,9 @@ int launch_loss_slope(int dtype, const ProductArgs& g, const LossArgs& loss, int
                            : prod::loss_slope_f32(g, loss, padded, kind, s, err);
 }
 
-int launch_product_onto(int dtype, const ProductArgs& g, const ProductPlan& plan, bool fresh, void* stream, std::string* err) {
+int launch_product_onto(int dtype, const ProductArgs& g, const ProductPlan& plan, void* stream, std::string* err) {
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  return dtype == CCL_BF16 ? prod::product_onto_bf16(g, plan, fresh, s, err) : prod::product_onto_f32(g, plan, fresh, s, err);
+  return dtype == CCL_BF16 ? prod::product_onto_bf16(g, plan, s, err) : prod::product_onto_f32(g, plan, s, err);
 }
 
 int launch_loss_rows(const LossRowsArgs& args, const LossArgs& loss, void* stream, std::string* err) {

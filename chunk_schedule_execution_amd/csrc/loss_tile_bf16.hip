@@ -11,8 +11,7 @@ int loss_slope_bf16(const ProductArgs& g, const LossArgs& loss, int64_t padded, 
                     std::string* err) {
   return launch_end<bf16, false>(g, LossSlope{loss, padded}, kind, 1, s, err);
 }
-int product_onto_bf16(const ProductArgs& g, const ProductPlan& plan, bool fresh, hipStream_t s, std::string* err) {
-  if (fresh) return launch_end<bf16, true>(g, Results(), plan.kind, plan.splits, s, err);
+int product_onto_bf16(const ProductArgs& g, const ProductPlan& plan, hipStream_t s, std::string* err) {
   return launch_end<bf16, true>(g, AddedSums(), plan.kind, plan.splits, s, err);
 }
 

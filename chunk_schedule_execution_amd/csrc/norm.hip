@@ -61,10 +61,6 @@ __device__ inline void lds_barrier() {
 }
 
 __device__ inline int64_t flat_block() { return int64_t(blockIdx.y) * gridDim.x + blockIdx.x; }
-inline dim3 flat_grid(int64_t n) {
-  const int64_t x = std::min<int64_t>(n, 1 << 20);
-  return dim3(unsigned(x), unsigned((n + x - 1) / x));
-}
 
 // How the threads share out rows of packs: R threads to a row, `Held` packs each, and as many
 // rows side by side as a workgroup of 256 holds. One wave to a row needs no barrier.

@@ -3,6 +3,7 @@
 
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <string>
@@ -23,6 +24,12 @@ inline int hip_status(const char* what, std::string* err) {
   if (e == hipSuccess) return CCL_OK;
   *err = std::string(what) + ": " + hipGetErrorString(e);
   return CCL_ERR_HIP;
+}
+
+// A grid of n workgroups: one dimension holds less than 2^32 threads.
+inline dim3 flat_grid(int64_t n) {
+  const int64_t x = std::min<int64_t>(n, 1 << 20);
+  return dim3(unsigned(x), unsigned((n + x - 1) / x));
 }
 
 __device__ inline float widen(bf16 v) { return float(v); }
