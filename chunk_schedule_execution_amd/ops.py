@@ -380,9 +380,12 @@ def _select_desc(logits, choices, score, groups, kept_groups, group_best, renorm
     if score not in SCORES:
         _refuse(f"unknown score {score!r}")
     tokens, experts = logits.shape
-    return capi.ccl_select_desc(DTYPES[logits.dtype], SCORES[score], tokens, experts, choices, groups,
-                                groups if kept_groups is None else kept_groups, group_best, int(bool(renormalise)),
-                                scale, _ld(logits, "logits"))
+    kept = groups if kept_groups is None else kept_groups
+    # a descriptor's fields hold 32 bits and would take the rest of a number for the whole
+    if not (1 <= kept <= groups <= 64 and 1 <= group_best <= 2):
+        _refuse(f"groups: 1 .. 64 wanted, of which 1 to all stay by their 1 or 2 best, not {groups}, {kept}, {group_best}")
+    return capi.ccl_select_desc(DTYPES[logits.dtype], SCORES[score], tokens, experts, choices, groups, kept, group_best,
+                                int(bool(renormalise)), scale, _ld(logits, "logits"))
 
 
 def expert_select(logits, choices, score="softmax", bias=None, groups=1, kept_groups=None, group_best=1,
@@ -516,7 +519,7 @@ def _loss_desc(x, w, targets, shard, device):
         _refuse("w: (vocabulary, in) wanted")
     rows, k = x.shape
     _like(w, "w", (w.shape[0], k), x.dtype, device)
-    if shard is not None and shard < 0:
+    if shard is not None and not 0 <= shard < 1 << 31:
         _refuse("shard: the vocabulary's index of w's first row wanted")
     pt = _packed(targets, "targets", (rows,), torch.int32, device)
     d = capi.ccl_cross_entropy_desc(DTYPES[x.dtype], 0, rows, k, w.shape[0], -1 if shard is None else shard,
