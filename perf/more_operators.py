@@ -180,8 +180,9 @@ def run_own(s):
         return ops.expert_select_backward(s["dgates"], s["logits"], s["ids"], score=s["score"],
                                           renormalise=s["renorm"], scale=s["scale"])
     if op == "norm":
-        return ops.layer_norm(s["x"], weight=s["w"], bias=s["b"], residual=s["r"], eps=s["eps"],
+        outs = ops.layer_norm(s["x"], weight=s["w"], bias=s["b"], residual=s["r"], eps=s["eps"],
                               save_stats=s["stats"])
+        return outs if isinstance(outs, tuple) else [outs]  # out alone: neither a residual nor statistics
     if op == "norm_backward":
         return ops.layer_norm_backward(s["dout"], s["x"], s["mean"], s["rstd"], weight=s["w"], dtotal=s["r"],
                                        bias=s["b"] is not None)
