@@ -532,13 +532,15 @@ def _loss_desc(x, w, targets, shard, device):
 def linear_cross_entropy(x, w, targets, shard=None, stream=None):
     """Cross entropy of the logits z = x w^T, which are not kept: x (rows, in), w (vocabulary,
     in), targets (rows,) int32 -> (loss, lse), (rows,) float32, with lse = log sum exp z and
-    loss = lse - z at the target. A row whose target is negative or past the vocabulary is
-    left out: loss 0, no gradient.
+    loss = lse - z at the target. A row whose target is negative or, without ``shard``, past the
+    vocabulary is left out: loss 0, no gradient.
 
     With ``shard``, w holds the rows of the vocabulary from that index on (one rank's share),
     and the call returns (lse, picked): lse over them, picked the target's logit, 0 where the
     target is another shard's. ``cross_entropy_join`` makes loss and lse of all shards' pairs,
-    gathered. Autograd does not see the call."""
+    gathered. No shard knows where the vocabulary ends: there only a negative target leaves its
+    row out, one past the vocabulary counts as a row with loss = lse. Autograd does not see the
+    call."""
     device = _first(x, "x")
     d, pt = _loss_desc(x, w, targets, shard, device)
     on = _on(device, stream)
@@ -557,7 +559,8 @@ def linear_cross_entropy(x, w, targets, shard=None, stream=None):
 
 def cross_entropy_join(lse, picked, targets, stream=None):
     """(loss, lse) over a whole vocabulary from its shards' lse and picked, (shards, rows)
-    float32 each: what an AllGather of ``linear_cross_entropy``'s results gives."""
+    float32 each: what an AllGather of ``linear_cross_entropy``'s results gives. A row whose
+    target is negative has loss 0; the vocabulary's end is not known here, either."""
     if not isinstance(lse, torch.Tensor) or lse.dim() != 2:
         _refuse("lse: (shards, rows) wanted")
     shards, rows = lse.shape

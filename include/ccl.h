@@ -769,11 +769,16 @@ typedef struct {
  * Cross entropy of z = x w^T against targets (int32 by row) without keeping z: lse = log sum
  * exp z over w's rows, picked = z at the target, loss = lse - picked, all fp32 by row. loss and
  * picked may be NULL. A row whose target is negative is left out: its loss is 0 and it has no
- * part in a gradient; of a whole vocabulary, so is a target past its end. With a shard, picked
- * is 0 for a target that is no row of it, and loss has to be NULL: ccl_cross_entropy_join gives
- * it from all shards' lse and picked. A logit of -inf is no part of lse; one that is NaN or +inf
- * makes its row's lse NaN. The workspace holds 8 bytes for 32 or 64 logits; of a small product
- * (16 rows at most, or one whose sums are split) its fp32 sums, below 256 MiB.
+ * part in a gradient. Of a whole vocabulary, so is a row whose target is past its end. A shard's
+ * call does not know that end: with a shard, picked is 0 for a target that is no row of it, and
+ * a target that is no shard's row leaves its row in, with loss = lse and a gradient without the
+ * - 1; rows to leave out need a negative target there. loss has to be NULL with a shard:
+ * ccl_cross_entropy_join gives it from all shards' lse and picked. A logit of -inf is no part of
+ * lse; one that is NaN or +inf makes its row's lse NaN.
+ * The workspace holds 8 bytes for 32 or 64 logits and 4 for a row, and copies of x and w where
+ * they do not lie on the 16-byte grid (base, row distance and in_features); for a small product
+ * (16 rows at most, or one whose sums are split) its fp32 sums instead, below 256 MiB, and what
+ * a product of its sizes copies.
  * Errors: INVALID_ARGUMENT, UNSUPPORTED (dtype), HIP; the gradient's and the join's too.
  */
 int64_t ccl_linear_cross_entropy_workspace(const ccl_cross_entropy_desc* desc, int backward);
@@ -782,17 +787,26 @@ int ccl_linear_cross_entropy(const ccl_cross_entropy_desc* desc, const void* x, 
                              void* stream);
 
 /* lse = log sum exp of the shards' lse_parts (shards x rows), loss = lse - the sum of their
- * picked_parts, 0 for a negative target. What an AllGather of the shards' sums is joined by. */
+ * picked_parts, 0 for a negative target (lse for one that is no shard's row: the end of the
+ * vocabulary is not known here). What an AllGather of the shards' sums is joined by. */
 int ccl_cross_entropy_join(int shards, int64_t rows, const float* lse_parts, const float* picked_parts,
                            const int32_t* targets, float* loss, float* lse, void* stream);
 
 /*
  * Gradients: dz = dloss (exp(z - lse) - [column is the target]), dx = dz w, dw = dz^T x. lse is
  * the whole vocabulary's (a shard's call gets the joined one; its dx is the shard's summand,
- * its dw its own). z is computed again, a piece of the vocabulary at a time: the workspace holds
- * dz of a piece, 512 MiB or 8192 columns of it. dz is rounded to the dtype for the two products,
- * as a stored gradient is; sums over pieces are fp32. A row left out has no part whatever its x,
- * dloss and lse hold, NaN included. dx or dw may be NULL.
+ * its dw its own). z is computed again, a piece of the vocabulary at a time. dz is rounded to the
+ * dtype for the two products, as a stored gradient is; sums over pieces are fp32. A row left out
+ * has no part whatever its x, dloss and lse hold, NaN included. dx or dw may be NULL.
+ * The workspace holds
+ *   - dz of a piece: 512 MiB or 8192 columns, up to 255 columns more;
+ *   - a copy of x, where dw is wanted or x is off the 16-byte grid;
+ *   - a copy of w where that is off it;
+ *   - the fp32 sums of dx over the pieces, where there are several and dx is wanted: rows x
+ *     in_features for each split of dx's product (16 at most);
+ *   - the fp32 sums of the largest other product that is split, or of a small product's logits.
+ * 65536 x 4096 over 131072 in bf16: 1 GiB for the loss; 2.5 GiB for both gradients, 2 for dx, 1.5
+ * for dw.
  */
 int ccl_linear_cross_entropy_backward(const ccl_cross_entropy_desc* desc, const float* dloss, const void* x,
                                       const void* w, const int32_t* targets, const float* lse, void* dx, void* dw,

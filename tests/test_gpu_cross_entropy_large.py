@@ -70,3 +70,24 @@ def test_cross_entropy_in_pieces_of_large_tiles(rows, k, vocabulary, pieces, spl
     alone = ops.linear_cross_entropy_backward(dloss, x, w, targets, lse, need_dw=False)[0]
     dx, _ = ops.linear_cross_entropy_backward(dloss, x, w, targets, lse)
     assert torch.equal(alone, dx)
+
+
+def test_targets_past_the_vocabulary_of_shards():
+    """The whole vocabulary leaves such rows out. Shards do not know its end: the rows count, with
+    loss = lse and a gradient without a target; negative targets leave them out of both."""
+    rows, k, vocabulary = 90, 64, 200
+    x, w, targets = inputs(47, rows, k, vocabulary, "bf16")
+    targets[:10] = torch.tensor([vocabulary, vocabulary + 1, 2**31 - 1, -1, -2**31] * 2, dtype=torch.int32)
+    past = targets >= vocabulary
+    whole, whole_lse = ops.linear_cross_entropy(x, w, targets)
+    assert not bool(whole[past].any())
+    parts = [ops.linear_cross_entropy(x, w[a:a + 100], targets, shard=a) for a in (0, 100)]
+    loss, lse = ops.cross_entropy_join(*(torch.stack([p[i] for p in parts]) for i in (0, 1)), targets)
+    assert torch.equal(loss[past], lse[past]) and not bool(loss[targets < 0].any())
+    dloss = normal(50, rows)
+    for a in (0, 100):
+        dx, _ = backward(x, w[a:a + 100], targets, lse, shard=a, dloss=dloss)
+        assert bool(dx[past].any(1).all()) and not bool(dx[targets < 0].any())
+    negative = torch.where(past, torch.full_like(targets, -1), targets)
+    loss, _ = ops.cross_entropy_join(*(torch.stack([p[i] for p in parts]) for i in (0, 1)), negative)
+    assert not bool(loss[past].any())
